@@ -47,11 +47,16 @@ C_SYMBOLS = (
     "kq_workspace_size", "kq_status_str", "kq_last_cuda_error", "kq_version",
     "kq_rht_quant_nvfp4_dynamic_noalloc", "kq_diag_tc_steps", "kq_diag_fail_next_launch",
     "kq_gemm_nvfp4", "kq_diag_tc_steps_f16",
+    "kq_gemv", "kq_attn_decode_int4_kv", "kq_attn_workspace_size", "kq_kv_copy_pages",
 )
 
 # Fixed device scratch of kq_rht_quant_nvfp4_dynamic_noalloc (see include/kq.h).
 KQ_NOALLOC_SCRATCH_BYTES = 1 << 20
 KQ_NOALLOC_MAX_TOKENS = (KQ_NOALLOC_SCRATCH_BYTES - 16) // 8
+
+# Limits of kq_gemv (see include/kq.h).
+KQ_GEMV_MAX_TOKENS = 16
+KQ_GEMV_MAX_K = 131072
 
 _lib = None
 
@@ -114,6 +119,16 @@ def lib() -> ctypes.CDLL:
     L.kq_diag_tc_steps_f16.restype = i32
     L.kq_gemm_nvfp4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, i32, vp]
     L.kq_gemm_nvfp4.restype = i32
+    L.kq_gemv.argtypes = [i32, vp, i32, i64, vp, vp, vp, vp, i64, i32, i32, vp, i32, vp]
+    L.kq_gemv.restype = i32
+    L.kq_attn_decode_int4_kv.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, i64,
+                                         vp, i64, i32, vp, i32, i32, ctypes.c_float, vp, vp, sz,
+                                         vp]
+    L.kq_attn_decode_int4_kv.restype = i32
+    L.kq_attn_workspace_size.argtypes = [i64, i32, i32]
+    L.kq_attn_workspace_size.restype = sz
+    L.kq_kv_copy_pages.argtypes = [vp, i64, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.kq_kv_copy_pages.restype = i32
     _lib = L
     return L
 
@@ -279,6 +294,143 @@ def kq_gemm_nvfp4(a_codes, a_scales, a_tensor_scale, b_codes, b_scales, b_tensor
            "kq_gemm_nvfp4")
 
 
+# ------------------------------------------------- decode-step operators
+def _want(t, what: str, dtype, shape, device=None) -> int:
+    """Device pointer of a contiguous CUDA tensor of this type and shape (on
+    this device); ValueError for anything else.  The kernels take sizes from
+    the shapes, so a wrong one would read or write out of bounds."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: kq functions take CUDA tensors (device pointers)")
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected {dtype} {list(shape)}, "
+                         f"got {t.dtype} {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: kq functions take contiguous tensors")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what}: on {t.device}, the call's tensors are on {device}")
+    return t.data_ptr()
+
+
+def _launch(fn, where: str, device, stream, *args) -> None:
+    """fn(*args, stream) with `device` current; its current stream when none is
+    given."""
+    cuda = _torch().cuda
+    if cuda.current_device() != device.index:
+        with cuda.device(device):
+            _check(fn(*args, _stream(stream)), where)
+    else:
+        _check(fn(*args, _stream(stream)), where)
+
+
+def kq_gemv(fmt: int, x, codes, scales, zeros, tensor_scale, group: int, y,
+            stream=None) -> None:
+    """y = x W^T for a few tokens: x [m, k] (m <= KQ_GEMV_MAX_TOKENS), W [n, k]
+    in a 4-bit format as kq_dequant takes it, y [m, n]; x and y fp32 or bf16."""
+    torch = _torch()
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ValueError("x is [m, k] and codes are [n, k/2]")
+    (m, k), n, dev = x.shape, codes.shape[0], x.device
+    if fmt == KQ_FMT_INT4_SYM:
+        kind, shape = torch.float32, (n,)
+    elif fmt == KQ_FMT_INT4_ASYM:
+        kind, shape = torch.float16, (n, k // 128)
+    elif fmt == KQ_FMT_NVFP4:
+        kind, shape = torch.uint8, (n, k // 16)
+    else:
+        kind, shape = torch.uint8, (n, k // 32)
+    asym, nv = fmt == KQ_FMT_INT4_ASYM, fmt == KQ_FMT_NVFP4
+    _launch(lib().kq_gemv, "kq_gemv", dev, stream, fmt,
+            _want(x, "x", x.dtype, (m, k)), _dtype_code(x), m,
+            _want(codes, "codes", torch.uint8, (n, k // 2), dev),
+            _want(scales, "scales", kind, shape, dev),
+            _want(zeros, "zeros", kind, shape, dev) if asym else None,
+            _want(tensor_scale, "tensor_scale", torch.float32, (1,), dev) if nv else None,
+            n, k, group, _want(y, "y", y.dtype, (m, n), dev), _dtype_code(y))
+
+
+class KVCacheInt4:
+    """The three arrays of a paged INT4 cache (keys or values) as
+    kq_rht_quant_int4_kv writes them: codes uint8 [num_slots, dim/2], scales
+    and zeros fp16 [num_slots, dim/128]; with one more leading dimension a
+    cache of several layers.  A view of the caller's tensors, checked once."""
+
+    __slots__ = ("codes", "scales", "zeros", "layers", "num_slots", "dim", "device", "layered")
+
+    def __init__(self, codes, scales, zeros):
+        torch = _torch()
+        if codes.dim() not in (2, 3):
+            raise ValueError("codes are [num_slots, dim/2] or [layers, num_slots, dim/2]")
+        lead, half = tuple(codes.shape[:-1]), codes.shape[-1]
+        if half % 64 != 0 or half == 0:
+            raise ValueError(f"codes: {half} bytes a row are not whole 128-wide heads")
+        _want(codes, "codes", torch.uint8, lead + (half,))
+        _want(scales, "scales", torch.float16, lead + (half // 64,), codes.device)
+        _want(zeros, "zeros", torch.float16, lead + (half // 64,), codes.device)
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.layered = len(lead) == 2
+        self.layers = lead[0] if self.layered else 1
+        self.num_slots, self.dim, self.device = lead[-1], 2 * half, codes.device
+
+    def layer(self, i: int) -> "KVCacheInt4":
+        """Layer i as a cache of its own (views of the same memory)."""
+        if not self.layered:
+            raise ValueError("the cache has no layers")
+        return KVCacheInt4(self.codes[i], self.scales[i], self.zeros[i])
+
+
+def kq_attn_decode_int4_kv(q, k_cache: KVCacheInt4, v_cache: KVCacheInt4, k_signs, v_signs,
+                           block_table, page_size: int, seq_lens, softmax_scale: float, out,
+                           workspace, window: int = 0, sinks: int = 0, stream=None) -> None:
+    """Attention of one new token per sequence over the paged INT4 caches: q and
+    out bf16 [batch, q_heads, 128], block_table int32 [batch, width], seq_lens
+    int32 [batch]; window > 0 keeps the last `window` tokens and the first
+    `sinks` ones visible.  workspace: empty_attn_workspace(...)."""
+    torch = _torch()
+    batch, q_heads, _ = q.shape
+    dev, dim = q.device, k_cache.dim
+    if k_cache.layered or v_cache.layered:
+        raise ValueError("the attention reads one layer: pass cache.layer(i)")
+    if (v_cache.dim, v_cache.num_slots) != (dim, k_cache.num_slots):
+        raise ValueError("the key and value caches differ in shape")
+    if k_cache.device != dev or v_cache.device != dev:
+        raise ValueError(f"the caches are not on {dev}")
+    shape = (batch, q_heads, 128)
+    _launch(lib().kq_attn_decode_int4_kv, "kq_attn_decode_int4_kv", dev, stream,
+            _want(q, "q", torch.bfloat16, shape), batch, q_heads, dim // 128,
+            None if k_signs is None else _want(k_signs, "k_signs", torch.int8, (dim,), dev),
+            None if v_signs is None else _want(v_signs, "v_signs", torch.int8, (dim,), dev),
+            k_cache.codes.data_ptr(), k_cache.scales.data_ptr(), k_cache.zeros.data_ptr(),
+            v_cache.codes.data_ptr(), v_cache.scales.data_ptr(), v_cache.zeros.data_ptr(),
+            k_cache.num_slots,
+            _want(block_table, "block_table", torch.int32, (batch, block_table.shape[1]), dev),
+            block_table.shape[1], page_size,
+            _want(seq_lens, "seq_lens", torch.int32, (batch,), dev), window, sinks,
+            softmax_scale, _want(out, "out", torch.bfloat16, shape, dev),
+            _want(workspace, "workspace", torch.uint8, tuple(workspace.shape), dev),
+            workspace.numel())
+
+
+def kq_kv_copy_pages(pairs, page_size: int, k_cache: KVCacheInt4,
+                     v_cache: Optional[KVCacheInt4] = None, stream=None) -> None:
+    """Copies pages of the cache(s): pairs int32 [n, 2] of (source, destination)
+    page; pairs with a page outside the cache are skipped."""
+    torch = _torch()
+    dev = k_cache.device
+    values = (None, None, None)
+    if v_cache is not None:
+        if (v_cache.dim, v_cache.num_slots, v_cache.layers) != \
+                (k_cache.dim, k_cache.num_slots, k_cache.layers):
+            raise ValueError("the key and value caches differ in shape")
+        if v_cache.device != dev:
+            raise ValueError(f"the caches are not both on {dev}")
+        values = (v_cache.codes.data_ptr(), v_cache.scales.data_ptr(), v_cache.zeros.data_ptr())
+    n = pairs.shape[0]
+    _launch(lib().kq_kv_copy_pages, "kq_kv_copy_pages", dev, stream,
+            _want(pairs, "pairs", torch.int32, (n, 2), dev), n, page_size, k_cache.num_slots,
+            k_cache.layers, k_cache.dim, k_cache.codes.data_ptr(), k_cache.scales.data_ptr(),
+            k_cache.zeros.data_ptr(), *values)
+
+
 def kq_dequant(fmt: int, codes, scales, zeros, tensor_scale, tokens: int, dim: int,
                group: int, out, stream=None) -> None:
     """Codes and scales back to fp32 (exact product, one rounding)."""
@@ -370,3 +522,23 @@ def empty_nvfp4(tokens: int, dim: int, block: int = 0, device="cuda", mma_layout
             scales,
             torch.empty((1,), dtype=torch.float32, device=device),
             torch.empty((max(ws, 16),), dtype=torch.uint8, device=device))
+
+
+def empty_kv_cache(num_slots: int, dim: int, layers: int = 0, device="cuda") -> KVCacheInt4:
+    """A KVCacheInt4 of num_slots rows (of `layers` layers when layers > 0)."""
+    import torch
+    lead = (layers, num_slots) if layers else (num_slots,)
+    return KVCacheInt4(torch.empty(lead + (dim // 2,), dtype=torch.uint8, device=device),
+                       torch.empty(lead + (dim // 128,), dtype=torch.float16, device=device),
+                       torch.empty(lead + (dim // 128,), dtype=torch.float16, device=device))
+
+
+def kq_attn_workspace_size(batch: int, q_heads: int, kv_heads: int) -> int:
+    return int(lib().kq_attn_workspace_size(batch, q_heads, kv_heads))
+
+
+def empty_attn_workspace(batch: int, q_heads: int, kv_heads: int, device="cuda"):
+    """Workspace of kq_attn_decode_int4_kv; one per call that may overlap."""
+    import torch
+    return torch.empty((max(kq_attn_workspace_size(batch, q_heads, kv_heads), 16),),
+                       dtype=torch.uint8, device=device)

@@ -359,6 +359,100 @@ KQ_API kq_status kq_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* a_scales,
   });
 }
 
+KQ_API kq_status kq_gemv(int fmt, const void* x, int x_dtype, int64_t m, const uint8_t* codes,
+                         const void* scales, const void* zeros, const float* tensor_scale,
+                         int64_t n, int k, int group, void* y, int y_dtype,
+                         kq_stream_t stream) {
+  if (m < 0 || n <= 0 || k <= 0) return KQ_ERR_INVALID_ARG;
+  if (m > 0 && (!x || !codes || !scales || !y)) return KQ_ERR_INVALID_ARG;
+  if ((x_dtype != KQ_F32 && x_dtype != KQ_BF16) || (y_dtype != KQ_F32 && y_dtype != KQ_BF16))
+    return KQ_ERR_UNSUPPORTED;
+  if (m > KQ_GEMV_MAX_TOKENS || n >= (int64_t(1) << 31) || k > KQ_GEMV_MAX_K || k % 32 != 0)
+    return KQ_ERR_UNSUPPORTED;
+  const kq_status st = check_dequant(fmt, codes, scales, zeros, tensor_scale, m, k, group, y);
+  if (st != KQ_OK) return st;
+  if (!aligned(x, 16) || (fmt == KQ_FMT_NVFP4 && !aligned(scales, 2))) return KQ_ERR_MISALIGNED;
+  if (m == 0) return KQ_OK;
+  return dispatch([&] {
+    return kq::launch_gemv(fmt, x, x_dtype == KQ_BF16 ? 1 : 0, (int)m, codes, scales, zeros,
+                           tensor_scale, n, k, y, y_dtype == KQ_BF16 ? 1 : 0,
+                           reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+// Head layouts of the decode attention.
+static bool attn_heads_ok(int64_t batch, int q_heads, int kv_heads) {
+  return batch >= 0 && batch <= 65535 && kv_heads >= 1 && kv_heads <= 128 && q_heads >= 1 &&
+         q_heads % kv_heads == 0 && q_heads / kv_heads <= 128;
+}
+
+KQ_API size_t kq_attn_workspace_size(int64_t batch, int q_heads, int kv_heads) {
+  return attn_heads_ok(batch, q_heads, kv_heads)
+             ? kq::attn_workspace_bytes(batch, q_heads, kv_heads) : 0;
+}
+
+KQ_API kq_status kq_attn_decode_int4_kv(
+    const void* q, int64_t batch, int q_heads, int kv_heads, const int8_t* k_signs,
+    const int8_t* v_signs, const uint8_t* k_codes, const uint16_t* k_scales,
+    const uint16_t* k_zeros, const uint8_t* v_codes, const uint16_t* v_scales,
+    const uint16_t* v_zeros, int64_t num_slots, const int32_t* block_table,
+    int64_t table_width, int page_size, const int32_t* seq_lens, int window, int sinks,
+    float softmax_scale, void* out, void* workspace, size_t ws_bytes, kq_stream_t stream) {
+  if (batch < 0 || num_slots < 0 || table_width < 0 || page_size <= 0 || window < 0 || sinks < 0)
+    return KQ_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale)) return KQ_ERR_INVALID_ARG;
+  constexpr int64_t kMost = int64_t(1) << 40;
+  if (!attn_heads_ok(batch, q_heads, kv_heads) || page_size > 65536 || num_slots >= kMost ||
+      table_width >= kMost || batch * table_width >= kMost)
+    return KQ_ERR_UNSUPPORTED;
+  if (batch > 0) {
+    if (!q || !out || !seq_lens || !workspace ||
+        ws_bytes < kq::attn_workspace_bytes(batch, q_heads, kv_heads))
+      return KQ_ERR_INVALID_ARG;
+    if (table_width > 0 && !block_table) return KQ_ERR_INVALID_ARG;
+    if (num_slots > 0 &&
+        (!k_codes || !k_scales || !k_zeros || !v_codes || !v_scales || !v_zeros))
+      return KQ_ERR_INVALID_ARG;
+  }
+  const void* wide[] = {q,        out,      workspace, k_signs, v_signs, k_codes,
+                        k_scales, k_zeros,  v_codes,   v_scales, v_zeros};
+  for (const void* p : wide)
+    if (!aligned(p, 16)) return KQ_ERR_MISALIGNED;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4)) return KQ_ERR_MISALIGNED;
+  if (batch == 0) return KQ_OK;
+  const kq::AttnArgs a{q,        batch,    q_heads, kv_heads,  k_signs,   v_signs,
+                       k_codes,  k_scales, k_zeros, v_codes,   v_scales,  v_zeros,
+                       num_slots, block_table, table_width, page_size, seq_lens,
+                       window,   sinks,    softmax_scale, out, workspace};
+  return dispatch(
+      [&] { return kq::launch_attn_decode(a, reinterpret_cast<cudaStream_t>(stream)); });
+}
+
+KQ_API kq_status kq_kv_copy_pages(const int32_t* pairs, int64_t n_pairs, int page_size,
+                                  int64_t num_slots, int layers, int dim, uint8_t* k_codes,
+                                  uint16_t* k_scales, uint16_t* k_zeros, uint8_t* v_codes,
+                                  uint16_t* v_scales, uint16_t* v_zeros, kq_stream_t stream) {
+  if (n_pairs < 0 || page_size <= 0 || num_slots < 0 || layers <= 0 || dim <= 0)
+    return KQ_ERR_INVALID_ARG;
+  if (dim % 128 != 0 || dim > 16384 || page_size > 65536 ||
+      num_slots >= (int64_t(1) << 40) / layers || n_pairs >= (int64_t(1) << 31) / layers)
+    return KQ_ERR_UNSUPPORTED;
+  const bool values = v_codes || v_scales || v_zeros;
+  if (n_pairs > 0 && (!pairs || !k_codes || !k_scales || !k_zeros)) return KQ_ERR_INVALID_ARG;
+  if (values && (!v_codes || !v_scales || !v_zeros)) return KQ_ERR_INVALID_ARG;
+  const void* wide[] = {k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros};
+  for (const void* p : wide)
+    if (!aligned(p, 16)) return KQ_ERR_MISALIGNED;
+  if (!aligned(pairs, 8)) return KQ_ERR_MISALIGNED;
+  if (n_pairs == 0 || num_slots < page_size) return KQ_OK;
+  uint8_t* const codes[2] = {k_codes, v_codes};
+  uint16_t* const small_[4] = {k_scales, k_zeros, v_scales, v_zeros};
+  return dispatch([&] {
+    return kq::launch_kv_copy(pairs, n_pairs, page_size, num_slots, layers, dim, codes, small_,
+                              values ? 2 : 1, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
 KQ_API kq_status kq_device_errors(unsigned int* flags) {
   if (!flags) return KQ_ERR_INVALID_ARG;
   cudaError_t e = kq::take_tc_errors(&flags[0]);
@@ -398,7 +492,7 @@ KQ_API int kq_last_cuda_error(void) { return g_last_cuda_error; }
 
 KQ_API void kq_diag_fail_next_launch(int cuda_error) { g_fail_next_launch = cuda_error; }
 
-KQ_API int kq_version(void) { return (1 << 16) | 1; }
+KQ_API int kq_version(void) { return (1 << 16) | 2; }
 
 static kq_status diag_tc_steps(const uint16_t* a, const uint16_t* b, float* d1, float* d2,
                                unsigned int* status, int fp16, kq_stream_t stream) {

@@ -42,6 +42,42 @@ cudaError_t launch_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* a_scales,
                               int64_t n, int64_t k, void* c, int c_bf16, cudaStream_t s);
 cudaError_t take_gemm_errors(unsigned int* out);
 
+// Products of a few tokens with 4-bit weights (kq_gemv.cu).
+cudaError_t launch_gemv(int fmt, const void* x, int x_bf16, int m, const uint8_t* codes,
+                        const void* scales, const void* zeros, const float* tscale, int64_t n,
+                        int k, void* y, int y_bf16, cudaStream_t s);
+
+// Decode attention over the paged INT4 cache (kq_attn.cu).
+struct AttnArgs {
+  const void* q;              // bf16 [batch, q_heads, 128]
+  int64_t batch;
+  int q_heads, kv_heads;
+  const int8_t* k_signs;
+  const int8_t* v_signs;
+  const uint8_t* k_codes;
+  const uint16_t* k_scales;
+  const uint16_t* k_zeros;
+  const uint8_t* v_codes;
+  const uint16_t* v_scales;
+  const uint16_t* v_zeros;
+  int64_t num_slots;
+  const int32_t* block_table;
+  int64_t table_width;
+  int page_size;
+  const int32_t* seq_lens;
+  int window, sinks;
+  float softmax_scale;
+  void* out;                  // bf16 [batch, q_heads, 128]
+  void* workspace;
+};
+size_t attn_workspace_bytes(int64_t batch, int q_heads, int kv_heads);
+cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
+
+// Pages of a paged INT4 cache copied to other pages (kq_kvcopy.cu).
+cudaError_t launch_kv_copy(const int32_t* pairs, int64_t n_pairs, int page_size,
+                           int64_t num_slots, int layers, int dim, uint8_t* const codes[2],
+                           uint16_t* const small_[4], int arrays, cudaStream_t s);
+
 // Records a CUDA error for kq_last_cuda_error() on the calling thread.
 void set_last_cuda_error(int err);
 

@@ -305,6 +305,105 @@ KQ_API kq_status kq_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* a_scales,
                                kq_stream_t stream);
 
 /*
+ * kq_gemv -- products of a few tokens with a 4-bit weight matrix, the linear
+ * layer of a decode step (QuaRot reviews, review 3 Questions: with Y = X H^T
+ * applied to activations and weights alike, X W^T is unchanged; NVFP4 thread,
+ * discrete_descent's note: INT4-g128, NVFP4 and MXFP4 weights):
+ *   y[j][i] = sum_k x[j][k] w[i][k],
+ * where w is what kq_dequant defines for the same fmt, codes, scales, zeros,
+ * tensor_scale and group.  No weight is rounded on the way (code times scale
+ * is exact in the arithmetic used); products are accumulated in fp32.
+ *   x       [m, k] fp32 or bf16 (x_dtype), 0 <= m <= KQ_GEMV_MAX_TOKENS; m == 0
+ *           is a no-op.  fp32 rows keep 22 significant bits.
+ *   codes   [n, k/2] bytes; scales, zeros, tensor_scale: as for kq_dequant with
+ *           tokens = n and dim = k (block scales row-major).
+ *   y       [m, n] fp32 or bf16 (y_dtype, rounded to nearest even).
+ * Supported: n >= 1 (any), 32 <= k <= KQ_GEMV_MAX_K with k % 32 == 0 (k % 128
+ * == 0 for KQ_FMT_INT4_ASYM, whose group is 128).  codes, x and y 16-byte
+ * aligned, scales and zeros at their element size (2 bytes for the NVFP4 block
+ * scales).  y may not alias an input.  Errors: KQ_ERR_INVALID_ARG,
+ * KQ_ERR_UNSUPPORTED, KQ_ERR_MISALIGNED, KQ_ERR_CUDA; nothing is launched on an
+ * error.  No workspace; results do not depend on the order of execution.
+ */
+#define KQ_GEMV_MAX_TOKENS 16
+#define KQ_GEMV_MAX_K 131072
+KQ_API kq_status kq_gemv(int fmt, const void* x, int x_dtype, int64_t m, const uint8_t* codes,
+                         const void* scales, const void* zeros, const float* tensor_scale,
+                         int64_t n, int k, int group, void* y, int y_dtype, kq_stream_t stream);
+
+/*
+ * kq_attn_decode_int4_kv -- attention of one new token per sequence over the
+ * paged key and value caches that kq_rht_quant_int4_kv writes (QuaRot reviews,
+ * final comments: the KV cache at 4 bits with a per-head 128-point Hadamard).
+ * The cache holds rotated heads, so the query is rotated on the way in and the
+ * result rotated back on the way out; both happen inside the call.  For
+ * sequence b and query head i, which reads cached head i / (q_heads / kv_heads):
+ *   q' = H_128 (k_signs * q) / sqrt(128)
+ *   a_t = softmax_scale * sum_d q'_d sk_t (uk_td - zk_t)      (visible t only)
+ *   o   = sum_t exp(a_t) sv_t (uv_t - zv_t) / sum_t exp(a_t)
+ *   out = v_signs * (H_128 o) / sqrt(128)
+ * Token t of sequence b is at cache row block_table[b][t / page_size] *
+ * page_size + t % page_size.  It is visible when t < seq_lens[b] and (window ==
+ * 0, or t < sinks, or t >= seq_lens[b] - window): the last `window` tokens and
+ * the `sinks` first ones.  The new token's own key and value are in the cache
+ * already and count in seq_lens.  Lengths below zero count as zero, lengths
+ * above table_width * page_size as that.  A token whose row lies outside
+ * [0, num_slots) is not visible; table entries of pages without a visible
+ * token are not read.  A sequence with no visible token gets zeros.  What lies
+ * in rows that are not visible, NaN included, does not matter.
+ *   q, out        bf16 [batch, q_heads, 128], 16-byte aligned; no alias.
+ *   k_signs, v_signs  int8 [kv_heads * 128] (the signs of the writing calls) or
+ *                 NULL, 16-byte aligned.
+ *   *_codes       [num_slots, kv_heads * 64] bytes; *_scales, *_zeros fp16
+ *                 [num_slots, kv_heads]; all 16-byte aligned.
+ *   block_table   int32 [batch, table_width]; seq_lens int32 [batch] (4-byte
+ *                 aligned, device memory).
+ *   workspace     kq_attn_workspace_size(batch, q_heads, kv_heads) bytes of
+ *                 device memory, 16-byte aligned.  Its contents on entry do not
+ *                 matter and are clobbered; calls that may overlap on the GPU
+ *                 (other streams, graphs replayed side by side) need one each.
+ * Supported: 1 <= kv_heads <= 128, q_heads a multiple of kv_heads with
+ * q_heads / kv_heads <= 128, 1 <= page_size <= 65536, window and sinks >= 0,
+ * softmax_scale finite, num_slots and batch * table_width below 2^40, batch <=
+ * 65535.  batch == 0 is a no-op.  The query and the softmax weights are held in
+ * fp16 with a power-of-two scale per head (relative rounding 2^-11) for the
+ * tensor cores; scores, maxima, sums and the accumulated values in fp32.
+ * Results do not depend on the order of execution.
+ */
+KQ_API kq_status kq_attn_decode_int4_kv(
+    const void* q, int64_t batch, int q_heads, int kv_heads, const int8_t* k_signs,
+    const int8_t* v_signs, const uint8_t* k_codes, const uint16_t* k_scales,
+    const uint16_t* k_zeros, const uint8_t* v_codes, const uint16_t* v_scales,
+    const uint16_t* v_zeros, int64_t num_slots, const int32_t* block_table,
+    int64_t table_width, int page_size, const int32_t* seq_lens, int window, int sinks,
+    float softmax_scale, void* out, void* workspace, size_t ws_bytes, kq_stream_t stream);
+
+/* Bytes of workspace kq_attn_decode_int4_kv needs (0 on bad arguments). */
+KQ_API size_t kq_attn_workspace_size(int64_t batch, int q_heads, int kv_heads);
+
+/*
+ * kq_kv_copy_pages -- copies pages of a paged INT4 cache to other pages, in
+ * every layer and all of its arrays in one launch: a forked sequence's last
+ * page, a pool compacted (QuaRot reviews, final comments: the KV cache at 4
+ * bits).  Page p is rows p * page_size ... of each layer.
+ *   pairs    int32 [n_pairs, 2] in device memory, 8-byte aligned: source and destination page.
+ *            A pair with either one outside [0, num_slots / page_size) is
+ *            skipped (padding), and so is one whose two pages are the same.
+ *   codes    [layers, num_slots, dim/2] bytes; scales, zeros fp16 [layers,
+ *            num_slots, dim/128]; 16-byte aligned.  The three value arrays may
+ *            all be NULL (one cache only).
+ * The pairs run at the same time: a destination that is also another pair's
+ * source, or two pairs with the same destination, leave that destination
+ * unspecified (nothing else is touched).  Rows of no destination are left as
+ * they are.  Supported: dim a multiple of 128 up to 16384, 1 <= page_size <=
+ * 65536, layers >= 1.  n_pairs == 0 is a no-op.
+ */
+KQ_API kq_status kq_kv_copy_pages(const int32_t* pairs, int64_t n_pairs, int page_size,
+                                  int64_t num_slots, int layers, int dim, uint8_t* k_codes,
+                                  uint16_t* k_scales, uint16_t* k_zeros, uint8_t* v_codes,
+                                  uint16_t* v_scales, uint16_t* v_zeros, kq_stream_t stream);
+
+/*
  * kq_device_errors -- failure reports of the tensor-core kernels.  Every
  * wait of those kernels is bounded (about two seconds); when one runs out the
  * kernel records it in its family's error word and returns without writing
