@@ -4,107 +4,830 @@
 // rotated, so the query is rotated on the way in (q . k is unchanged when both
 // carry the rotation) and the result rotated back on the way out.
 //
-// One CTA per (sequence, query head), a thread per token for the scores and a
-// thread per dimension for the values, with a running maximum and sum.
+// Mathematics.  With codes u, scales s and zero points z of a token's head,
+//   a_t = f s_t (sum_d q_d u_td - z_t sum_d q_d),   p_t = 2^(a_t - max a)
+//   o_d = (sum_t (p_t s'_t) u_td - sum_t (p_t s'_t) z'_t) / sum_t p_t
+// so both products run on the bare 4-bit codes: a code masked out of its word
+// IS an fp16 number (u 2^-24, or 16 u 2^-24 for the upper nibble of a byte: an
+// fp16 bit pattern is linear up to 11 bits), exact on the tensor cores, and
+// costs 5 integer operations per 8 codes.  The factor 16 of the odd
+// dimensions is taken out of the query (keys) and the result (values).
+//
+// Bound by HBM: each visible token is read once, 68 bytes a head for the key
+// and 68 for the value.  mma.sync (m16n8k16) carries the contraction: its 16
+// rows are tokens (scores) or dimensions (values), its 8 columns the query
+// heads that share the cached head, and at the memory's rate it needs 3/8 of
+// that path's throughput; the accumulators stay where the softmax is computed.
+//
+// Work split.  The visible tokens of all (sequence, head block, column chunk)
+// units are cut into tiles, and the tiles dealt to the CTAs in contiguous
+// ranges of equal length, computed on the device from seq_lens: long and short
+// sequences load the machine alike and nothing depends on host knowledge of
+// the lengths.  A unit that one CTA covers is finished there; the others leave
+// partial sums in the workspace, which a second small kernel (launched as a
+// programmatic dependent) joins in CTA order.
+//
+// Per CTA: warp 8 copies the tiles' code rows into shared stages (bulk copies,
+// a row of all the block's heads each), warp 9 their scales and zero points,
+// eight warps compute, each its own head (or its own part of the tokens when
+// there are fewer heads).  Stage rows are 32 bytes longer than a multiple of
+// 128, which makes both fragment reads free of bank conflicts.  Every wait is
+// bounded.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <cstdint>
 
 #include "kq_internal.h"
+#include "kq_sm100.cuh"
 
 namespace kq {
 namespace at {
 
-__global__ void __launch_bounds__(128) k_attn(AttnArgs P) {
-  __shared__ float qs[128], ps[128];
-  __shared__ double red[40];
-  __shared__ int64_t slots[128];
-  const int d = threadIdx.x;
-  const int64_t b = blockIdx.x;
-  const int h = blockIdx.y, kh = h / (P.q_heads / P.kv_heads);
-  auto rotate = [&] {                 // unnormalized H_128 of qs
-    for (int st = 1; st < 128; st <<= 1) {
-      __syncthreads();
-      const float a = qs[d], c = qs[d ^ st];
-      __syncthreads();
-      qs[d] = (d & st) ? c - a : a + c;
-    }
-    __syncthreads();
-  };
-  const int64_t qi = (b * P.q_heads + h) * 128 + d;
-  float q = __bfloat162float(static_cast<const __nv_bfloat16*>(P.q)[qi]);
-  if (P.k_signs && P.k_signs[kh * 128 + d] < 0) q = -q;
-  qs[d] = q * 0.08838834764831845f;
-  rotate();
-  int64_t len = P.seq_lens[b];
-  const int64_t most = P.table_width * P.page_size;
-  len = len < 0 ? 0 : len > most ? most : len;
+using namespace sm100;
+
+constexpr int kWarps = 8;                     // compute warps
+constexpr int kThreads = 32 * (kWarps + 2);
+constexpr int kCols = 8;                      // query heads a unit carries
+constexpr int kMaxCtas = 320;
+constexpr int kMinTiles = 2;                  // tiles a CTA takes at least
+constexpr int kPartFloats = kCols * 128 + 2 * kCols;   // o, m, l of one head
+
+__device__ unsigned int g_attn_error = 0;
+
+// A warp waits together, and gives up together.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_attn_error));
+}
+
+// Tokens of one sequence: positions v < vis, v + skip from `sinks` on.
+struct Seq {
+  int vis, skip;
+};
+__device__ __forceinline__ Seq sequence(const AttnArgs& P, int most, int64_t b) {
+  const int len = min(max(__ldg(P.seq_lens + b), 0), most);
   const int64_t keep = (int64_t)P.window + P.sinks;
-  const int64_t skip = P.window > 0 && len > keep ? len - keep : 0;
-  const int64_t vis = len - skip;
-  const int row = P.kv_heads;
-  float m = -INFINITY, l = 0.0f, o = 0.0f;
-  for (int64_t t0 = 0; t0 < vis; t0 += 128) {
-    __syncthreads();
-    int64_t slot = -1;
-    const int64_t v = t0 + d;
-    if (v < vis) {
-      const int64_t pos = v < P.sinks ? v : v + skip;
-      const int64_t page = P.block_table[b * P.table_width + pos / P.page_size];
-      slot = page * P.page_size + pos % P.page_size;
-      if (page < 0 || slot >= P.num_slots) slot = -1;
+  Seq s;
+  s.skip = P.window > 0 && len > keep ? (int)(len - keep) : 0;
+  s.vis = len - s.skip;
+  return s;
+}
+__device__ __forceinline__ int longest(const AttnArgs& P) {
+  const int64_t most = P.table_width * P.page_size;
+  return most > 0x7fffffff ? 0x7fffffff : (int)most;
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Tiles of the sequences before `upto` (a warp together).
+__device__ __forceinline__ int64_t tiles_before(const AttnArgs& P, int most, int tile,
+                                                int64_t upto) {
+  int64_t n = 0;
+  for (int64_t b = threadIdx.x & 31; b < upto; b += 32)
+    n += (sequence(P, most, b).vis + tile - 1) / tile;
+  return warp_sum(n);
+}
+
+// The CTAs that share `total` tiles, and the first tile of CTA c.
+__device__ __forceinline__ int ctas_used(int64_t total, int grid) {
+  const int64_t c = total / kMinTiles;
+  return c < 1 ? 1 : c > grid ? grid : (int)c;
+}
+__device__ __forceinline__ int64_t cta_first(int64_t total, int ctas, int64_t c) {
+  return c * total / ctas;
+}
+
+// A walk over a CTA's tiles: unit (b, sub) and tile within it.
+struct Walk {
+  int64_t b;
+  int sub, tile, tiles;
+  Seq seq;
+};
+template <int TILE>
+__device__ __forceinline__ void next_sequence(const AttnArgs& P, int most, Walk& w) {
+  do {
+    ++w.b;
+    w.seq = sequence(P, most, w.b);
+    w.tiles = (w.seq.vis + TILE - 1) / TILE;
+  } while (w.tiles == 0);
+}
+// The walk at unit tile `first` (a warp together; first < the total).
+template <int TILE>
+__device__ __forceinline__ Walk find(const AttnArgs& P, int most, int subs, int64_t first) {
+  const int lane = threadIdx.x & 31;
+  int64_t base = 0;                      // tiles of all the sequences before this round
+  Walk w{};
+  for (int64_t b0 = 0; b0 < P.batch; b0 += 32) {
+    const int64_t b = b0 + lane;
+    const int n = b < P.batch ? (sequence(P, most, b).vis + TILE - 1) / TILE : 0;
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
     }
-    float sc = -INFINITY;
-    if (slot >= 0) {
-      const uint8_t* c = P.k_codes + (slot * row + kh) * 64;
-      const float s = f16_bits_to_f32(P.k_scales[slot * row + kh]);
-      const float z = f16_bits_to_f32(P.k_zeros[slot * row + kh]);
-      float a = 0.0f;
-      for (int i = 0; i < 64; ++i) {
-        const uint32_t w = c[i];
-        a = fmaf(qs[2 * i], (float)(w & 15u) - z, a);
-        a = fmaf(qs[2 * i + 1], (float)(w >> 4) - z, a);
+    const unsigned hit = __ballot_sync(0xffffffffu, (base + incl) * subs > first);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      const int64_t before = __shfl_sync(0xffffffffu, base + incl - n, l);
+      w.b = b0 + l;
+      w.seq = sequence(P, most, w.b);
+      w.tiles = (w.seq.vis + TILE - 1) / TILE;
+      const int64_t off = first - before * subs;
+      w.sub = (int)(off / w.tiles);
+      w.tile = (int)(off - (int64_t)w.sub * w.tiles);
+      return w;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return w;
+}
+
+// Cache row of visible token v, -1 where there is none.
+__device__ __forceinline__ int64_t cache_row(const AttnArgs& P, const Walk& w, int v) {
+  if (v >= w.seq.vis) return -1;
+  const uint32_t pos = (uint32_t)(v < P.sinks ? v : v + w.seq.skip);
+  const uint32_t page_in = pos / (uint32_t)P.page_size;
+  const int64_t page = __ldg(P.block_table + w.b * P.table_width + page_in);
+  const int64_t row = page * P.page_size + (pos - page_in * (uint32_t)P.page_size);
+  return page < 0 || row >= P.num_slots ? -1 : row;
+}
+
+template <int HB>
+struct Shape {
+  static constexpr int kSplit = kWarps / HB;             // warps a head
+  static constexpr int kTok = HB == 1 ? 16 : 32;         // tokens a warp and tile
+  static constexpr int kTile = kTok * kSplit;            // tokens a tile
+  static constexpr int kRow = HB * 64 + 32;              // bytes a staged code row
+  static constexpr int kCodes = kTile * kRow;            // keys or values of a tile
+  static constexpr int kScales = HB * kTile * 8;         // (sk, zk, sv, zv) halves
+  static constexpr int kStage = 2 * kCodes + kScales;
+  static constexpr int kStages = HB == 8 ? 3 : HB == 1 ? 3 : 2;
+  // the warps of a head are joined two by two: one writes, one adds
+  static constexpr int kJoin = kSplit > 1 ? kWarps / 2 * kPartFloats * 4 : 0;
+  static constexpr size_t kSmem = kStages * kStage + kJoin + 2 * kStages * 8;
+};
+
+__device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t bytes,
+                                         uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+               "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ float exp2_(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max_over_rows(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float sum_over_rows(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+// 16 dimensions a lane (16 (lane / 4) + i): unnormalized H_128 over the 8 lanes.
+__device__ __forceinline__ void hadamard_rows(float (&v)[16]) {
+#pragma unroll
+  for (int st = 1; st < 16; st <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!(i & st)) {
+        const float a = v[i], b = v[i | st];
+        v[i] = a + b;
+        v[i | st] = a - b;
       }
-      sc = a * s * P.softmax_scale;
-    }
-    slots[d] = slot;
-    const float mt = fmaxf(m, block_max(sc, red));
-    const float ref = mt == -INFINITY ? 0.0f : mt;
-    const float keep_f = expf(m - ref);
-    const float p = expf(sc - ref);
-    ps[d] = p;
-    l = l * keep_f + (float)block_sum_d((double)p, red);
-    o *= keep_f;
-    m = mt;
-    __syncthreads();
-    const int n = vis - t0 < 128 ? (int)(vis - t0) : 128;
-    for (int t = 0; t < n; ++t) {
-      const int64_t sl = slots[t];
-      if (sl < 0) continue;
-      const uint32_t w = P.v_codes[(sl * row + kh) * 64 + d / 2];
-      const float u = (float)((d & 1) ? w >> 4 : w & 15u);
-      o = fmaf(ps[t], (u - f16_bits_to_f32(P.v_zeros[sl * row + kh])) *
-                          f16_bits_to_f32(P.v_scales[sl * row + kh]), o);
+#pragma unroll
+  for (int st = 4; st < 32; st <<= 1) {
+    const bool up = (threadIdx.x & st) != 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float o = __shfl_xor_sync(0xffffffffu, v[i], st);
+      v[i] = up ? o - v[i] : v[i] + o;
     }
   }
+}
+// Rotates 16 values a lane back, applies the signs and stores them as bf16.
+__device__ __forceinline__ void store_result(const AttnArgs& P, float (&v)[16], int64_t b, int qh,
+                                             int kh, bool store) {
+  hadamard_rows(v);
+  const int d0 = 16 * ((threadIdx.x & 31) >> 2);
+  uint32_t w[8];
+  uint4 sg = make_uint4(0, 0, 0, 0);
+  if (P.v_signs) sg = __ldg(reinterpret_cast<const uint4*>(P.v_signs + kh * 128 + d0));
+  const uint32_t s4[4] = {sg.x, sg.y, sg.z, sg.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float r[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int e = 2 * i + j;
+      const uint32_t neg = s4[e >> 2] << (24 - 8 * (e & 3)) & 0x80000000u;
+      r[j] = __uint_as_float(__float_as_uint(v[e] * 0.08838834764831845f) ^ neg);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(r[0], r[1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  if (store) {
+    uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) +
+                                         (b * P.q_heads + qh) * 128 + d0);
+    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+template <int HB>
+__global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
+  using S = Shape<HB>;
+  constexpr int TILE = S::kTile, MB = S::kTok / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* join = reinterpret_cast<float*>(smem + S::kStages * S::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStage + S::kJoin);
+  uint64_t* empty = full + S::kStages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1 + 32);
+      mbar_init(&empty[s], kWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   __syncthreads();
-  qs[d] = l > 0.0f ? o / l * 0.08838834764831845f : 0.0f;
-  rotate();
-  float r = qs[d];
-  if (P.v_signs && P.v_signs[kh * 128 + d] < 0) r = -r;
-  static_cast<__nv_bfloat16*>(P.out)[qi] = __float2bfloat16_rn(r);
+
+  const int most = longest(P);
+  const int group = P.q_heads / P.kv_heads, chunks = (group + kCols - 1) / kCols;
+  const int subs = P.kv_heads / HB * chunks;
+  const int64_t total = tiles_before(P, most, TILE, P.batch) * subs;
+  if (total == 0) return;
+  const int ctas = ctas_used(total, gridDim.x);
+  if ((int)blockIdx.x >= ctas) return;
+  const int64_t first = cta_first(total, ctas, blockIdx.x);
+  const int64_t count = cta_first(total, ctas, blockIdx.x + 1) - first;
+  Walk w = find<TILE>(P, most, subs, first);
+
+  auto step = [&](Walk& x) {
+    if (++x.tile == x.tiles) {
+      x.tile = 0;
+      if (++x.sub == subs) {
+        x.sub = 0;
+        next_sequence<TILE>(P, most, x);
+      }
+    }
+  };
+
+  if (warp == kWarps) {
+    // ================= code rows, by bulk copies
+    constexpr int N = TILE / 32;
+    int64_t row[N];
+    auto rows = [&] {
+#pragma unroll
+      for (int j = 0; j < N; ++j) row[j] = cache_row(P, w, w.tile * TILE + j * 32 + lane);
+    };
+    rows();
+    int64_t it = 0;
+    for (; it < count; ++it) {
+      const int s = (int)(it % S::kStages);
+      if (it >= S::kStages && !wait(&empty[s], (uint32_t)(it / S::kStages - 1) & 1)) break;
+      const int64_t head0 = (int64_t)(w.sub / chunks) * HB;
+      int valid = 0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) valid += __popc(__ballot_sync(0xffffffffu, row[j] >= 0));
+      if (lane == 0) mbar_expect_tx(&full[s], (uint32_t)valid * 2 * HB * 64);
+      __syncwarp();
+      const uint32_t base = smem_u32(smem + s * S::kStage);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (row[j] >= 0) {
+          const int64_t off = (row[j] * P.kv_heads + head0) * 64;
+          const uint32_t dst = base + (uint32_t)(j * 32 + lane) * S::kRow;
+          bulk_row(dst, P.k_codes + off, HB * 64, &full[s]);
+          bulk_row(dst + S::kCodes, P.v_codes + off, HB * 64, &full[s]);
+        }
+      if (it + 1 < count) {
+        step(w);
+        rows();
+      }
+    }
+    // no copy may still be in flight when the CTA exits
+    for (int64_t j = it > S::kStages ? it - S::kStages : 0; j < it; ++j)
+      wait(&full[j % S::kStages], (uint32_t)(j / S::kStages) & 1);
+  } else if (warp == kWarps + 1) {
+    // ================= scales and zero points: (sk, zk, sv, zv) a token and head
+    constexpr int N = TILE / 32;
+    struct Loaded {
+      uint16_t v[4][HB];
+    };
+    Loaded cur[N];
+    const uint16_t* src[4] = {P.k_scales, P.k_zeros, P.v_scales, P.v_zeros};
+    auto load = [&] {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int64_t r = cache_row(P, w, w.tile * TILE + j * 32 + lane);
+        const int64_t off = r * P.kv_heads + (int64_t)(w.sub / chunks) * HB;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          if (r >= 0) {
+            if constexpr (HB == 8) {
+              *reinterpret_cast<uint4*>(cur[j].v[a]) =
+                  __ldg(reinterpret_cast<const uint4*>(src[a] + off));
+            } else if constexpr (HB == 4) {
+              *reinterpret_cast<uint2*>(cur[j].v[a]) =
+                  __ldg(reinterpret_cast<const uint2*>(src[a] + off));
+            } else if constexpr (HB == 2) {
+              *reinterpret_cast<uint32_t*>(cur[j].v[a]) =
+                  __ldg(reinterpret_cast<const uint32_t*>(src[a] + off));
+            } else {
+              cur[j].v[a][0] = __ldg(src[a] + off);
+            }
+          } else {
+            // a token that is not visible: NaN in the key scale marks it, the
+            // rest is zero so that nothing of it reaches a sum
+#pragma unroll
+            for (int h = 0; h < HB; ++h) cur[j].v[a][h] = a == 0 ? 0x7fff : 0;
+          }
+        }
+      }
+    };
+    load();
+    for (int64_t it = 0; it < count; ++it) {
+      const int s = (int)(it % S::kStages);
+      if (it >= S::kStages && !wait(&empty[s], (uint32_t)(it / S::kStages - 1) & 1)) break;
+      uint2* to = reinterpret_cast<uint2*>(smem + s * S::kStage + 2 * S::kCodes);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int h = 0; h < HB; ++h)
+          to[h * TILE + j * 32 + lane] =
+              make_uint2(cur[j].v[0][h] | (uint32_t)cur[j].v[1][h] << 16,
+                         cur[j].v[2][h] | (uint32_t)cur[j].v[3][h] << 16);
+      mbar_arrive(&full[s]);
+      if (it + 1 < count) {
+        step(w);
+        load();
+      }
+    }
+  } else {
+    // ================= compute: head `hw` of the block, tokens tok0 .. of a tile
+    const int hw = warp / S::kSplit, part = warp % S::kSplit;
+    const int tok0 = part * S::kTok;
+    const int g = lane >> 2, t = lane & 3;
+    // the tokens of accumulator rows 2t and 2t + 1, and of row g
+    const int even = t, odd = 4 + ((t + 2) & 3);
+    const int mine = g & 1 ? 4 + (((g >> 1) + 2) & 3) : g >> 1;
+    uint32_t qf[4][4];
+    float fa[2], fz[2];                    // per column 2t, 2t + 1
+    float m[2], l[2], zs[2], o[8][4];
+    int ev = 0;
+    int64_t it = 0;
+    int segment = 0;
+    bool ok = true;                        // false: a wait ran out, nothing more is stored
+    while (it < count) {
+      // ---- the unit's query, rotated; lane (g, t) holds dimensions 32 t .. of column g
+      const int kh = w.sub / chunks * HB + hw;
+      const int col0 = w.sub % chunks * kCols;
+      const int columns = min(kCols, group - col0);
+      {
+        float q[32];
+        if (g < columns) {
+          const uint4* from = reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(P.q) +
+              (w.b * P.q_heads + (int64_t)kh * group + col0 + g) * 128 + 32 * t);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = __ldg(from + i);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              q[8 * i + 2 * j] = __uint_as_float(x[j] << 16);
+              q[8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
+            }
+          }
+          if (P.k_signs) {
+            const uint4* sp = reinterpret_cast<const uint4*>(P.k_signs + kh * 128 + 32 * t);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 v = __ldg(sp + i);
+              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const uint32_t neg = x[j >> 2] << (24 - 8 * (j & 3)) & 0x80000000u;
+                q[16 * i + j] = __uint_as_float(__float_as_uint(q[16 * i + j]) ^ neg);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) q[i] = 0.0f;
+        }
+#pragma unroll
+        for (int st = 1; st < 32; st <<= 1)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(i & st)) {
+              const float a = q[i], b = q[i | st];
+              q[i] = a + b;
+              q[i | st] = a - b;
+            }
+        float top = 0.0f;
+#pragma unroll
+        for (int st = 1; st < 4; st <<= 1)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float v = __shfl_xor_sync(0xffffffffu, q[i], st);
+            q[i] = (lane & st) ? v - q[i] : q[i] + v;
+          }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(q[i]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // fp16 with a power of two per column that puts its largest element in
+        // [2^14, 2^15): 11 significant bits over 28 binades
+        const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+        const int sh = top > 0.0f ? min(max(14 - ex, -100), 100) : 0;
+        const float up = pow2f(sh);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float lo = q[8 * i + j] * up, hi = q[8 * i + 4 + j] * up;
+            qf[i][j] = half2_bits(lo, hi);
+            const float2 r = half2_floats(qf[i][j]);
+            sum += r.x + r.y;
+            if (j & 1) qf[i][j] = half2_bits(r.x * 0.0625f, r.y * 0.0625f);
+          }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const float f = P.softmax_scale * (1.4426950408889634f * 0.08838834764831845f) * pow2f(-sh);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float fj = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4);
+          fa[j] = fj * 0x1p24f;
+          fz[j] = fj * __shfl_sync(0xffffffffu, sum, (2 * t + j) * 4);
+          m[j] = -INFINITY;
+          l[j] = zs[j] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+        ev = -30;
+      }
+      const int64_t todo = min((int64_t)(w.tiles - w.tile), count - it);
+      for (int64_t end = it + todo; it < end; ++it) {
+        const int s = (int)(it % S::kStages);
+        ok = ok && wait(&full[s], (uint32_t)(it / S::kStages) & 1);
+        if (!ok) continue;
+        const uint8_t* kb = smem + s * S::kStage + tok0 * S::kRow + hw * 64;
+        const uint8_t* vb = kb + S::kCodes;
+        const uint2* sb = reinterpret_cast<const uint2*>(smem + s * S::kStage + 2 * S::kCodes) +
+                          hw * TILE + tok0;
+        float sc[MB][2][2];                // [block][row g or g + 8][column]
+        uint2 sz[MB][2];
+        float tmax[2] = {-INFINITY, -INFINITY};
+        uint32_t vmax = 0;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          const uint4 ka = *reinterpret_cast<const uint4*>(kb + (mb * 16 + mine) * S::kRow + t * 16);
+          const uint4 kc =
+              *reinterpret_cast<const uint4*>(kb + (mb * 16 + 8 + mine) * S::kRow + t * 16);
+          const uint32_t xa[4] = {ka.x, ka.y, ka.z, ka.w}, xc[4] = {kc.x, kc.y, kc.z, kc.w};
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mma16816(c, xa[i] & 0x000f000fu, xc[i] & 0x000f000fu, xa[i] & 0x00f000f0u,
+                     xc[i] & 0x00f000f0u, qf[i][0], qf[i][1]);
+            const uint32_t ya = xa[i] >> 8, yc = xc[i] >> 8;
+            mma16816(c, ya & 0x000f000fu, yc & 0x000f000fu, ya & 0x00f000f0u, yc & 0x00f000f0u,
+                     qf[i][2], qf[i][3]);
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            sz[mb][r] = sb[mb * 16 + 8 * r + mine];
+            const float2 k2 = half2_floats(sz[mb][r].x);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float a = k2.x * (fa[j] * c[2 * r + j] - k2.y * fz[j]);
+              sc[mb][r][j] = k2.x == k2.x ? a : -INFINITY;
+              tmax[j] = fmaxf(tmax[j], sc[mb][r][j]);
+            }
+            vmax = max(vmax, sz[mb][r].y & 0x7fffu);
+          }
+        }
+        // ---- running maximum and sum; the value scales' power of two
+        float ref[2], keep[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float mt = fmaxf(m[j], max_over_rows(tmax[j]));
+          ref[j] = mt == -INFINITY ? 0.0f : mt;
+          keep[j] = exp2_(m[j] - ref[j]);
+          m[j] = mt;
+          l[j] *= keep[j];
+        }
+        // value scales below 2^e of the largest seen: p s' 2^(15 - e) < 2^15 keeps
+        // 11 bits for weights down to 2^-29 and none is lost above 2^-39
+        vmax = redux_max(vmax);
+        const int e = vmax == 0 ? -30 : vmax < 0x400u ? -14 : (int)(vmax >> 10) - 14;
+        if (e > ev) {
+          const float down = pow2f(ev - e);
+          keep[0] *= down;
+          keep[1] *= down;
+          ev = e;
+        }
+        if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] *= keep[j & 1];
+          zs[0] *= keep[0];
+          zs[1] *= keep[1];
+        }
+        const float vup = pow2f(15 - ev);
+        uint32_t pf[MB][2];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 v2 = half2_floats(sz[mb][r].y);
+            const float p0 = exp2_(sc[mb][r][0] - ref[0]), p1 = exp2_(sc[mb][r][1] - ref[1]);
+            l[0] += p0;
+            l[1] += p1;
+            const float vs = v2.x * vup;
+            const uint32_t h = half2_bits(p0 * vs, p1 * vs);
+            const float2 rr = half2_floats(h);
+            zs[0] += rr.x * v2.y;
+            zs[1] += rr.y * v2.y;
+            pf[mb][r] = transpose8x8(h);
+          }
+        // ---- values
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          uint2 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = *reinterpret_cast<const uint2*>(
+                vb + (mb * 16 + 8 * (i >> 1) + (i & 1 ? odd : even)) * S::kRow + g * 8);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {     // 4 dimensions of the lane's 16
+            const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+            const uint32_t y01 = j < 2 ? __byte_perm(x[0].x, x[1].x, sel)
+                                       : __byte_perm(x[0].y, x[1].y, sel);
+            const uint32_t y23 = j < 2 ? __byte_perm(x[2].x, x[3].x, sel)
+                                       : __byte_perm(x[2].y, x[3].y, sel);
+            mma16816(o[2 * j], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
+                     y23 & 0x00f000f0u, pf[mb][0], pf[mb][1]);
+            const uint32_t h01 = y01 >> 8, h23 = y23 >> 8;
+            mma16816(o[2 * j + 1], h01 & 0x000f000fu, h01 & 0x00f000f0u, h23 & 0x000f000fu,
+                     h23 & 0x00f000f0u, pf[mb][0], pf[mb][1]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+      }
+      // ---- end of the unit in this CTA: values in real units
+      float r[2][16];
+      {
+        const float down = pow2f(ev - 15);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          l[j] = sum_over_rows(l[j]);
+          const float z = sum_over_rows(zs[j]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            r[j][2 * i] = (o[i][j] * 0x1p24f - z) * down;
+            r[j][2 * i + 1] = (o[i][2 + j] * 0x1p20f - z) * down;
+          }
+        }
+      }
+      if constexpr (S::kSplit > 1) {
+        // join the head's warps, two by two
+#pragma unroll
+        for (int half = S::kSplit / 2; half > 0; half >>= 1) {
+          float* slot = join + (hw * (S::kSplit / 2) + part % half) * kPartFloats;
+          if (part >= half && part < 2 * half) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float4* to = reinterpret_cast<float4*>(slot + (2 * t + j) * 128 + 16 * g);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                to[i] = make_float4(r[j][4 * i], r[j][4 * i + 1], r[j][4 * i + 2], r[j][4 * i + 3]);
+              slot[kCols * 128 + 2 * t + j] = m[j];
+              slot[kCols * 128 + kCols + 2 * t + j] = l[j];
+            }
+          }
+          asm volatile("bar.sync 1, %0;" :: "n"(32 * kWarps) : "memory");
+          if (part < half) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float m2 = slot[kCols * 128 + 2 * t + j];
+              const float mt = fmaxf(m[j], m2), rf = mt == -INFINITY ? 0.0f : mt;
+              const float a = exp2_(m[j] - rf), b = exp2_(m2 - rf);
+              const float4* from = reinterpret_cast<const float4*>(slot + (2 * t + j) * 128 + 16 * g);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 v = from[i];
+                r[j][4 * i] = r[j][4 * i] * a + v.x * b;
+                r[j][4 * i + 1] = r[j][4 * i + 1] * a + v.y * b;
+                r[j][4 * i + 2] = r[j][4 * i + 2] * a + v.z * b;
+                r[j][4 * i + 3] = r[j][4 * i + 3] * a + v.w * b;
+              }
+              l[j] = l[j] * a + slot[kCols * 128 + kCols + 2 * t + j] * b;
+              m[j] = mt;
+            }
+          }
+          asm volatile("bar.sync 1, %0;" :: "n"(32 * kWarps) : "memory");
+        }
+      }
+      const bool whole = todo == w.tiles;
+      if (part == 0 && ok) {
+        if (whole) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float inv = l[j] > 0.0f ? 1.0f / l[j] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[j][i] *= inv;
+            store_result(P, r[j], w.b, kh * group + col0 + 2 * t + j, kh, 2 * t + j < columns);
+          }
+        } else {
+          float* slot = static_cast<float*>(P.workspace) +
+                        (((int64_t)blockIdx.x * 2 + (segment ? 1 : 0)) * kWarps + hw) * kPartFloats;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (2 * t + j < columns) {
+              float4* to = reinterpret_cast<float4*>(slot + (2 * t + j) * 128 + 16 * g);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                to[i] = make_float4(r[j][4 * i], r[j][4 * i + 1], r[j][4 * i + 2], r[j][4 * i + 3]);
+              if (g == 0) {
+                slot[kCols * 128 + 2 * t + j] = m[j];
+                slot[kCols * 128 + kCols + 2 * t + j] = l[j];
+              }
+            }
+        }
+      }
+      ++segment;
+      if (it < count) {
+        w.tile += (int)todo - 1;
+        step(w);
+      }
+    }
+  }
+}
+
+// Joins the partial sums of the units that more than one CTA worked on, in CTA
+// order, and writes zeros for the sequences without a visible token.  A CTA of
+// kJoinWarps warps takes one (sequence, query head): a lane holds 4 dimensions
+// and the warps share the partial sums.
+constexpr int kJoinWarps = 16;
+template <int HB>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) {
+  constexpr int TILE = Shape<HB>::kTile;
+  __shared__ float part_m[kMaxCtas], part_l[kMaxCtas], red[kJoinWarps][128];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t b = blockIdx.x;
+  const int qh = blockIdx.y, group = P.q_heads / P.kv_heads;
+  const int chunks = (group + kCols - 1) / kCols, kh = qh / group;
+  const int subs = P.kv_heads / HB * chunks;
+  const int sub = kh / HB * chunks + (qh - kh * group) / kCols, col = (qh - kh * group) % kCols;
+  const int most = longest(P);
+  const int tiles = (sequence(P, most, b).vis + TILE - 1) / TILE;
+  if (tiles == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x < 64)
+      reinterpret_cast<uint32_t*>(P.out)[(b * P.q_heads + qh) * 64 + threadIdx.x] = 0;
+    return;
+  }
+  const int64_t total = tiles_before(P, most, TILE, P.batch) * subs;
+  const int64_t u0 = tiles_before(P, most, TILE, b) * subs + (int64_t)sub * tiles;
+  const int ctas = ctas_used(total, grid);
+  const int c0 = (int)(((u0 + 1) * ctas - 1) / total);
+  const int c1 = (int)(((u0 + tiles) * ctas - 1) / total);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 == c1) return;
+  const int n = c1 - c0 + 1;
+  auto slot = [&](int i) {
+    const int64_t c = c0 + i;
+    const int second = cta_first(total, ctas, c) < u0 ? 1 : 0;
+    return static_cast<const float*>(P.workspace) +
+           ((c * 2 + second) * kWarps + kh % HB) * kPartFloats;
+  };
+  for (int i = threadIdx.x; i < n; i += 32 * kJoinWarps) {
+    const float* s = slot(i);
+    part_m[i] = s[kCols * 128 + col];
+    part_l[i] = s[kCols * 128 + kCols + col];
+  }
+  __syncthreads();
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, part_m[i]);
+  top = warp_max(top);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int i = warp; i < n; i += kJoinWarps) {
+    const float f = exp2_(part_m[i] - ref);
+    const float4 v = *reinterpret_cast<const float4*>(slot(i) + col * 128 + 4 * lane);
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+  }
+  *reinterpret_cast<float4*>(&red[warp][4 * lane]) = acc;
+  __syncthreads();
+  if (warp == 0) {
+    float l = 0.0f;
+    for (int i = lane; i < n; i += 32) l += part_l[i] * exp2_(part_m[i] - ref);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int g = lane >> 2;
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kJoinWarps; ++k) sum += red[k][16 * g + i];
+      v[i] = sum * inv;
+    }
+    store_result(P, v, b, qh, kh, (lane & 3) == 0);
+  }
+}
+
+template <int HB>
+cudaError_t launch(const AttnArgs& P, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute((const void*)k_attn<HB>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)Shape<HB>::kSmem);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+  k_attn<HB><<<grid, kThreads, Shape<HB>::kSmem, s>>>(P);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)P.batch, (unsigned)P.q_heads);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_join<HB>, P, grid);
 }
 
 }  // namespace at
 
 size_t attn_workspace_bytes(int64_t batch, int q_heads, int kv_heads) {
-  (void)batch; (void)q_heads; (void)kv_heads;
-  return 16;
+  (void)batch;
+  (void)q_heads;
+  (void)kv_heads;
+  return sizeof(float) * (size_t)at::kMaxCtas * 2 * at::kWarps * at::kPartFloats;
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& P, cudaStream_t s) {
-  at::k_attn<<<dim3((unsigned)P.batch, (unsigned)P.q_heads), 128, 0, s>>>(P);
-  return cudaGetLastError();
+  // the widest block of heads whose rows and scales stay whole
+  if (P.kv_heads % 8 == 0) return at::launch<8>(P, s);
+  if (P.kv_heads % 4 == 0) return at::launch<4>(P, s);
+  if (P.kv_heads % 2 == 0) return at::launch<2>(P, s);
+  return at::launch<1>(P, s);
+}
+
+// Reads and clears the error word of the attention kernel (device-synchronous).
+cudaError_t take_attn_errors(unsigned int* out) {
+  const unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, at::g_attn_error, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(at::g_attn_error, &zero, sizeof(unsigned int));
 }
 
 }  // namespace kq
