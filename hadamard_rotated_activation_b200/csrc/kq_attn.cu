@@ -27,8 +27,9 @@
 // partial sums in the workspace, which a second small kernel (launched as a
 // programmatic dependent) joins in CTA order.
 //
-// Per CTA: warp 8 copies the tiles' code rows into shared stages (bulk copies,
-// a row of all the block's heads each), warp 9 their scales and zero points,
+// Per CTA: warp 8 copies the tiles' code rows into shared stages (16-byte
+// asynchronous copies: rows lie anywhere, and bulk copies issued lane by lane
+// cost 100 cycles each, 6500 a tile, which bounded the kernel), warp 9 their scales and zero points,
 // eight warps compute, each its own head (or its own part of the tokens when
 // there are fewer heads).  Stage rows are 32 bytes longer than a multiple of
 // 128, which makes both fragment reads free of bank conflicts.  Every wait is
@@ -91,13 +92,31 @@ __device__ __forceinline__ int64_t tiles_before(const AttnArgs& P, int most, int
   return warp_sum(n);
 }
 
-// The CTAs that share `total` tiles, and the first tile of CTA c.
-__device__ __forceinline__ int ctas_used(int64_t total, int grid) {
-  const int64_t c = total / kMinTiles;
-  return c < 1 ? 1 : c > grid ? grid : (int)c;
+// How `total` tiles are dealt: `ctas` contiguous ranges, the first `more` of
+// them one tile longer than `each`.
+struct Deal {
+  int64_t each;
+  int ctas, more;
+};
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  // 32-bit division where it reaches (a 64-bit one costs several hundred cycles)
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
-__device__ __forceinline__ int64_t cta_first(int64_t total, int ctas, int64_t c) {
-  return c * total / ctas;
+__device__ __forceinline__ Deal deal(int64_t total, int grid) {
+  Deal d;
+  const int64_t c = total / kMinTiles;
+  d.ctas = c < 1 ? 1 : c > grid ? grid : (int)c;
+  d.each = div64(total, d.ctas);
+  d.more = (int)(total - d.each * d.ctas);
+  return d;
+}
+__device__ __forceinline__ int64_t cta_first(const Deal& d, int c) {
+  return c * d.each + min(c, d.more);
+}
+__device__ __forceinline__ int cta_of(const Deal& d, int64_t tile) {
+  const int64_t longer = (d.each + 1) * d.more;
+  return tile < longer ? (int)div64(tile, d.each + 1)
+                       : d.more + (int)div64(tile - longer, d.each);
 }
 
 // A walk over a CTA's tiles: unit (b, sub) and tile within it.
@@ -137,7 +156,7 @@ __device__ __forceinline__ Walk find(const AttnArgs& P, int most, int subs, int6
       w.seq = sequence(P, most, w.b);
       w.tiles = (w.seq.vis + TILE - 1) / TILE;
       const int64_t off = first - before * subs;
-      w.sub = (int)(off / w.tiles);
+      w.sub = (int)div64(off, w.tiles);
       w.tile = (int)(off - (int64_t)w.sub * w.tiles);
       return w;
     }
@@ -171,10 +190,13 @@ struct Shape {
   static constexpr size_t kSmem = kStages * kStage + kJoin + 2 * kStages * 8;
 };
 
-__device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t bytes,
-                                         uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+// Arrives (once a lane) when all of the lane's copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -274,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&full[s], 1 + 32);
+      mbar_init(&full[s], 64);
       mbar_init(&empty[s], kWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -286,10 +308,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
   const int subs = P.kv_heads / HB * chunks;
   const int64_t total = tiles_before(P, most, TILE, P.batch) * subs;
   if (total == 0) return;
-  const int ctas = ctas_used(total, gridDim.x);
-  if ((int)blockIdx.x >= ctas) return;
-  const int64_t first = cta_first(total, ctas, blockIdx.x);
-  const int64_t count = cta_first(total, ctas, blockIdx.x + 1) - first;
+  const Deal dl = deal(total, gridDim.x);
+  if ((int)blockIdx.x >= dl.ctas) return;
+  const int64_t first = cta_first(dl, blockIdx.x);
+  const int64_t count = cta_first(dl, blockIdx.x + 1) - first;
   Walk w = find<TILE>(P, most, subs, first);
 
   auto step = [&](Walk& x) {
@@ -303,41 +325,43 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
   };
 
   if (warp == kWarps) {
-    // ================= code rows, by bulk copies
+    // ================= code rows, 16 bytes a lane
     constexpr int N = TILE / 32;
+    constexpr int LANES = HB * 4;          // lanes a row
     int64_t row[N];
     auto rows = [&] {
 #pragma unroll
       for (int j = 0; j < N; ++j) row[j] = cache_row(P, w, w.tile * TILE + j * 32 + lane);
     };
     rows();
-    int64_t it = 0;
-    for (; it < count; ++it) {
+    const int64_t pitch = (int64_t)P.kv_heads * 64;
+    for (int64_t it = 0; it < count; ++it) {
       const int s = (int)(it % S::kStages);
       if (it >= S::kStages && !wait(&empty[s], (uint32_t)(it / S::kStages - 1) & 1)) break;
-      const int64_t head0 = (int64_t)(w.sub / chunks) * HB;
-      int valid = 0;
-#pragma unroll
-      for (int j = 0; j < N; ++j) valid += __popc(__ballot_sync(0xffffffffu, row[j] >= 0));
-      if (lane == 0) mbar_expect_tx(&full[s], (uint32_t)valid * 2 * HB * 64);
-      __syncwarp();
-      const uint32_t base = smem_u32(smem + s * S::kStage);
+      const int64_t off0 = (int64_t)(w.sub / chunks) * HB * 64 + 16 * (lane % LANES);
+      const uint32_t dst0 = smem_u32(smem + s * S::kStage) + lane / LANES * S::kRow +
+                            16 * (lane % LANES);
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        if (row[j] >= 0) {
-          const int64_t off = (row[j] * P.kv_heads + head0) * 64;
-          const uint32_t dst = base + (uint32_t)(j * 32 + lane) * S::kRow;
-          bulk_row(dst, P.k_codes + off, HB * 64, &full[s]);
-          bulk_row(dst + S::kCodes, P.v_codes + off, HB * 64, &full[s]);
+#pragma unroll 8
+        for (int i = 0; i < LANES; ++i) {
+          const int tok = i * (32 / LANES) + lane / LANES;
+          const int64_t r = __shfl_sync(0xffffffffu, row[j], tok);
+          if (r >= 0) {
+            const int64_t off = off0 + r * pitch;
+            const uint32_t dst = dst0 + (uint32_t)(j * 32 + i * (32 / LANES)) * S::kRow;
+            copy16(dst, P.k_codes + off);
+            copy16(dst + S::kCodes, P.v_codes + off);
+          }
         }
+      arrive_after_copies(&full[s]);
       if (it + 1 < count) {
         step(w);
         rows();
       }
     }
     // no copy may still be in flight when the CTA exits
-    for (int64_t j = it > S::kStages ? it - S::kStages : 0; j < it; ++j)
-      wait(&full[j % S::kStages], (uint32_t)(j / S::kStages) & 1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kWarps + 1) {
     // ================= scales and zero points: (sk, zk, sv, zv) a token and head
     constexpr int N = TILE / 32;
@@ -346,11 +370,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
     };
     Loaded cur[N];
     const uint16_t* src[4] = {P.k_scales, P.k_zeros, P.v_scales, P.v_zeros};
+    int64_t row[N];
+    int64_t head0;
+    auto rows = [&] {
+      head0 = (int64_t)(w.sub / chunks) * HB;
+#pragma unroll
+      for (int j = 0; j < N; ++j) row[j] = cache_row(P, w, w.tile * TILE + j * 32 + lane);
+    };
     auto load = [&] {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const int64_t r = cache_row(P, w, w.tile * TILE + j * 32 + lane);
-        const int64_t off = r * P.kv_heads + (int64_t)(w.sub / chunks) * HB;
+        const int64_t r = row[j];
+        const int64_t off = r * P.kv_heads + head0;
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
           if (r >= 0) {
@@ -375,7 +406,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
         }
       }
     };
+    // the rows are looked up one tile further ahead than the scales are loaded
+    rows();
     load();
+    if (count > 1) {
+      step(w);
+      rows();
+    }
     for (int64_t it = 0; it < count; ++it) {
       const int s = (int)(it % S::kStages);
       if (it >= S::kStages && !wait(&empty[s], (uint32_t)(it / S::kStages - 1) & 1)) break;
@@ -388,9 +425,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
               make_uint2(cur[j].v[0][h] | (uint32_t)cur[j].v[1][h] << 16,
                          cur[j].v[2][h] | (uint32_t)cur[j].v[3][h] << 16);
       mbar_arrive(&full[s]);
-      if (it + 1 < count) {
+      if (it + 1 < count) load();
+      if (it + 2 < count) {
         step(w);
-        load();
+        rows();
       }
     }
   } else {
@@ -470,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
         // fp16 with a power of two per column that puts its largest element in
         // [2^14, 2^15): 11 significant bits over 28 binades
         const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-        const int sh = top > 0.0f ? min(max(14 - ex, -100), 100) : 0;
+        const int sh = top > 0.0f ? min(max(14 - ex, -120), 120) : 0;
         const float up = pow2f(sh);
         float sum = 0.0f;
 #pragma unroll
@@ -705,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
 // order, and writes zeros for the sequences without a visible token.  A CTA of
 // kJoinWarps warps takes one (sequence, query head): a lane holds 4 dimensions
 // and the warps share the partial sums.
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 8;
 template <int HB>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) {
   constexpr int TILE = Shape<HB>::kTile;
@@ -718,25 +756,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
   const int sub = kh / HB * chunks + (qh - kh * group) / kCols, col = (qh - kh * group) % kCols;
   const int most = longest(P);
   const int tiles = (sequence(P, most, b).vis + TILE - 1) / TILE;
+  int64_t before = 0, all = 0;
+  for (int64_t i = lane; i < P.batch; i += 32) {
+    const int n = (sequence(P, most, i).vis + TILE - 1) / TILE;
+    all += n;
+    before += i < b ? n : 0;
+  }
+  const Deal dl = deal(warp_sum(all) * subs, grid);
+  const int64_t u0 = warp_sum(before) * subs + (int64_t)sub * tiles;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tiles == 0) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x < 64)
       reinterpret_cast<uint32_t*>(P.out)[(b * P.q_heads + qh) * 64 + threadIdx.x] = 0;
     return;
   }
-  const int64_t total = tiles_before(P, most, TILE, P.batch) * subs;
-  const int64_t u0 = tiles_before(P, most, TILE, b) * subs + (int64_t)sub * tiles;
-  const int ctas = ctas_used(total, grid);
-  const int c0 = (int)(((u0 + 1) * ctas - 1) / total);
-  const int c1 = (int)(((u0 + tiles) * ctas - 1) / total);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c0 == c1) return;
-  const int n = c1 - c0 + 1;
+  const int c0 = cta_of(dl, u0), n = cta_of(dl, u0 + tiles - 1) - c0 + 1;
+  if (n == 1) return;
+  // CTA c0 has its second slot for this unit unless it begins with it
+  const int second = cta_first(dl, c0) < u0 ? 1 : 0;
+  const float* base = static_cast<const float*>(P.workspace) +
+                      ((int64_t)c0 * 2 * kWarps + kh % HB) * kPartFloats;
   auto slot = [&](int i) {
-    const int64_t c = c0 + i;
-    const int second = cta_first(total, ctas, c) < u0 ? 1 : 0;
-    return static_cast<const float*>(P.workspace) +
-           ((c * 2 + second) * kWarps + kh % HB) * kPartFloats;
+    return base + (i * 2 + (i == 0 ? second : 0)) * kWarps * kPartFloats;
   };
   for (int i = threadIdx.x; i < n; i += 32 * kJoinWarps) {
     const float* s = slot(i);
@@ -749,7 +790,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
   top = warp_max(top);
   const float ref = top == -INFINITY ? 0.0f : top;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
   for (int i = warp; i < n; i += kJoinWarps) {
     const float f = exp2_(part_m[i] - ref);
     const float4 v = *reinterpret_cast<const float4*>(slot(i) + col * 128 + 4 * lane);
