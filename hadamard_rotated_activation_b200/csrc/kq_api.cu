@@ -402,8 +402,8 @@ KQ_API kq_status kq_attn_decode_int4_kv(
     return KQ_ERR_INVALID_ARG;
   if (!std::isfinite(softmax_scale)) return KQ_ERR_INVALID_ARG;
   constexpr int64_t kMost = int64_t(1) << 40;
-  if (!attn_heads_ok(batch, q_heads, kv_heads) || page_size > 65536 || num_slots >= kMost ||
-      table_width >= kMost || batch * table_width >= kMost)
+  if (!attn_heads_ok(batch, q_heads, kv_heads) || page_size > 65536 ||
+      num_slots >= (int64_t(1) << 31) || table_width >= kMost || batch * table_width >= kMost)
     return KQ_ERR_UNSUPPORTED;
   if (batch > 0) {
     if (!q || !out || !seq_lens || !workspace ||

@@ -49,6 +49,9 @@ using namespace sm100;
 
 constexpr int kWarps = 8;                     // compute warps
 constexpr int kThreads = 32 * (kWarps + 2);
+// A running maximum is kept until a score passes it by more than this (in
+// powers of two); the weights stay below 2^kSlack.
+constexpr int kSlack = 6;
 constexpr int kCols = 8;                      // query heads a unit carries
 constexpr int kMaxCtas = 320;
 constexpr int kMinTiles = 2;                  // tiles a CTA takes at least
@@ -82,14 +85,6 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
-}
-// Tiles of the sequences before `upto` (a warp together).
-__device__ __forceinline__ int64_t tiles_before(const AttnArgs& P, int most, int tile,
-                                                int64_t upto) {
-  int64_t n = 0;
-  for (int64_t b = threadIdx.x & 31; b < upto; b += 32)
-    n += (sequence(P, most, b).vis + tile - 1) / tile;
-  return warp_sum(n);
 }
 
 // How `total` tiles are dealt: `ctas` contiguous ranges, the first `more` of
@@ -133,46 +128,70 @@ __device__ __forceinline__ void next_sequence(const AttnArgs& P, int most, Walk&
     w.tiles = (w.seq.vis + TILE - 1) / TILE;
   } while (w.tiles == 0);
 }
-// The walk at unit tile `first` (a warp together; first < the total).
+// Tiles of sequence b0 + lane (0 behind the last one) and their inclusive sum
+// over the lanes (at most 2^26 tiles a sequence).
 template <int TILE>
-__device__ __forceinline__ Walk find(const AttnArgs& P, int most, int subs, int64_t first) {
+__device__ __forceinline__ void scan32(const AttnArgs& P, int most, int64_t b0, Seq& seq,
+                                       uint32_t& n, uint32_t& incl) {
   const int lane = threadIdx.x & 31;
-  int64_t base = 0;                      // tiles of all the sequences before this round
-  Walk w{};
-  for (int64_t b0 = 0; b0 < P.batch; b0 += 32) {
-    const int64_t b = b0 + lane;
-    const int n = b < P.batch ? (sequence(P, most, b).vis + TILE - 1) / TILE : 0;
-    int64_t incl = n;
+  seq = Seq{0, 0};
+  if (b0 + lane < P.batch) seq = sequence(P, most, b0 + lane);
+  n = incl = (uint32_t)(seq.vis + TILE - 1) / TILE;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+}
+// Deals the tiles and starts the CTA's walk; false when nothing is left for it.
+template <int TILE>
+__device__ __forceinline__ bool begin(const AttnArgs& P, int most, int subs, Walk& w,
+                                      int64_t& count) {
+  Seq seq;
+  uint32_t n, incl;
+  scan32<TILE>(P, most, 0, seq, n, incl);
+  int64_t total = __shfl_sync(0xffffffffu, incl, 31);
+  for (int64_t b0 = 32; b0 < P.batch; b0 += 32) {
+    Seq other;
+    uint32_t k, sum;
+    scan32<TILE>(P, most, b0, other, k, sum);
+    total += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  total *= subs;
+  if (total == 0) return false;
+  const Deal dl = deal(total, gridDim.x);
+  if ((int)blockIdx.x >= dl.ctas) return false;
+  const int64_t first = cta_first(dl, blockIdx.x);
+  count = cta_first(dl, blockIdx.x + 1) - first;
+  int64_t base = 0;
+  for (int64_t b0 = 0; b0 < P.batch; b0 += 32) {
+    if (b0 > 0) scan32<TILE>(P, most, b0, seq, n, incl);
     const unsigned hit = __ballot_sync(0xffffffffu, (base + incl) * subs > first);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      const int64_t before = __shfl_sync(0xffffffffu, base + incl - n, l);
       w.b = b0 + l;
-      w.seq = sequence(P, most, w.b);
-      w.tiles = (w.seq.vis + TILE - 1) / TILE;
+      w.seq.vis = __shfl_sync(0xffffffffu, seq.vis, l);
+      w.seq.skip = __shfl_sync(0xffffffffu, seq.skip, l);
+      w.tiles = (int)__shfl_sync(0xffffffffu, n, l);
+      const int64_t before = base + __shfl_sync(0xffffffffu, incl, l) - w.tiles;
       const int64_t off = first - before * subs;
       w.sub = (int)div64(off, w.tiles);
       w.tile = (int)(off - (int64_t)w.sub * w.tiles);
-      return w;
+      return true;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  return w;
+  return false;
 }
 
 // Cache row of visible token v, -1 where there is none.
-__device__ __forceinline__ int64_t cache_row(const AttnArgs& P, const Walk& w, int v) {
+__device__ __forceinline__ int cache_row(const AttnArgs& P, const Walk& w, int v) {
   if (v >= w.seq.vis) return -1;
   const uint32_t pos = (uint32_t)(v < P.sinks ? v : v + w.seq.skip);
   const uint32_t page_in = pos / (uint32_t)P.page_size;
   const int64_t page = __ldg(P.block_table + w.b * P.table_width + page_in);
   const int64_t row = page * P.page_size + (pos - page_in * (uint32_t)P.page_size);
-  return page < 0 || row >= P.num_slots ? -1 : row;
+  return page < 0 || row >= P.num_slots ? -1 : (int)row;
 }
 
 template <int HB>
@@ -190,8 +209,10 @@ struct Shape {
   static constexpr size_t kSmem = kStages * kStage + kJoin + 2 * kStages * 8;
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+// 16 bytes, or zeros (and no read) for bytes = 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // Arrives (once a lane) when all of the lane's copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
@@ -306,13 +327,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
   const int most = longest(P);
   const int group = P.q_heads / P.kv_heads, chunks = (group + kCols - 1) / kCols;
   const int subs = P.kv_heads / HB * chunks;
-  const int64_t total = tiles_before(P, most, TILE, P.batch) * subs;
-  if (total == 0) return;
-  const Deal dl = deal(total, gridDim.x);
-  if ((int)blockIdx.x >= dl.ctas) return;
-  const int64_t first = cta_first(dl, blockIdx.x);
-  const int64_t count = cta_first(dl, blockIdx.x + 1) - first;
-  Walk w = find<TILE>(P, most, subs, first);
+  Walk w;
+  int64_t count = 0;
+  const bool any = begin<TILE>(P, most, subs, w, count);
+  if (warp == kWarps + 1) {
+    // sequences without a visible token have no tile: their rows are zeros
+    for (int64_t b = blockIdx.x; b < P.batch; b += gridDim.x)
+      if (sequence(P, most, b).vis == 0)
+        for (int i = lane; i < P.q_heads * 16; i += 32)
+          reinterpret_cast<uint4*>(P.out)[b * P.q_heads * 16 + i] = make_uint4(0, 0, 0, 0);
+  }
+  if (!any) return;
 
   auto step = [&](Walk& x) {
     if (++x.tile == x.tiles) {
@@ -328,37 +353,38 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
     // ================= code rows, 16 bytes a lane
     constexpr int N = TILE / 32;
     constexpr int LANES = HB * 4;          // lanes a row
-    int64_t row[N];
+    const uint32_t dst0 = smem_u32(smem) + lane / LANES * S::kRow + 16 * (lane % LANES);
+    const int64_t pitch = (int64_t)P.kv_heads * 64;
+    int row[N];
     auto rows = [&] {
 #pragma unroll
       for (int j = 0; j < N; ++j) row[j] = cache_row(P, w, w.tile * TILE + j * 32 + lane);
     };
     rows();
-    const int64_t pitch = (int64_t)P.kv_heads * 64;
     for (int64_t it = 0; it < count; ++it) {
       const int s = (int)(it % S::kStages);
-      if (it >= S::kStages && !wait(&empty[s], (uint32_t)(it / S::kStages - 1) & 1)) break;
       const int64_t off0 = (int64_t)(w.sub / chunks) * HB * 64 + 16 * (lane % LANES);
-      const uint32_t dst0 = smem_u32(smem + s * S::kStage) + lane / LANES * S::kRow +
-                            16 * (lane % LANES);
+      const uint32_t dst = dst0 + s * S::kStage;
+      int now[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) now[j] = row[j];
+      if (it + 1 < count) {                // the next tile's rows, while this one is copied
+        step(w);
+        rows();
+      }
+      if (it >= S::kStages && !wait(&empty[s], (uint32_t)(it / S::kStages - 1) & 1)) break;
 #pragma unroll
       for (int j = 0; j < N; ++j)
 #pragma unroll 8
         for (int i = 0; i < LANES; ++i) {
-          const int tok = i * (32 / LANES) + lane / LANES;
-          const int64_t r = __shfl_sync(0xffffffffu, row[j], tok);
-          if (r >= 0) {
-            const int64_t off = off0 + r * pitch;
-            const uint32_t dst = dst0 + (uint32_t)(j * 32 + i * (32 / LANES)) * S::kRow;
-            copy16(dst, P.k_codes + off);
-            copy16(dst + S::kCodes, P.v_codes + off);
-          }
+          const int r = __shfl_sync(0xffffffffu, now[j], i * (32 / LANES) + lane / LANES);
+          const int64_t off = off0 + max(r, 0) * pitch;
+          const uint32_t to = dst + (uint32_t)(j * 32 + i * (32 / LANES)) * S::kRow;
+          const uint32_t bytes = r >= 0 ? 16 : 0;
+          copy16(to, P.k_codes + off, bytes);
+          copy16(to + S::kCodes, P.v_codes + off, bytes);
         }
       arrive_after_copies(&full[s]);
-      if (it + 1 < count) {
-        step(w);
-        rows();
-      }
     }
     // no copy may still be in flight when the CTA exits
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -370,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
     };
     Loaded cur[N];
     const uint16_t* src[4] = {P.k_scales, P.k_zeros, P.v_scales, P.v_zeros};
-    int64_t row[N];
+    int row[N];
     int64_t head0;
     auto rows = [&] {
       head0 = (int64_t)(w.sub / chunks) * HB;
@@ -380,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
     auto load = [&] {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const int64_t r = row[j];
-        const int64_t off = r * P.kv_heads + head0;
+        const int r = row[j];
+        const int64_t off = (int64_t)r * P.kv_heads + head0;
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
           if (r >= 0) {
@@ -441,8 +467,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
     const int mine = g & 1 ? 4 + (((g >> 1) + 2) & 3) : g >> 1;
     uint32_t qf[4][4];
     float fa[2], fz[2];                    // per column 2t, 2t + 1
-    float m[2], l[2], zs[2], o[8][4];
+    float m[2], ref[2], l[2], zs[2], o[8][4];
     int ev = 0;
+    uint32_t vlimit = 0;                   // fp16 bits of 2^ev
     int64_t it = 0;
     int segment = 0;
     bool ok = true;                        // false: a wait ran out, nothing more is stored
@@ -536,7 +563,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
         for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-        ev = -30;
+        ref[0] = ref[1] = 0.0f;
+        ev = -14;
+        vlimit = 0x400u;
       }
       const int64_t todo = min((int64_t)(w.tiles - w.tile), count - it);
       for (int64_t end = it + todo; it < end; ++it) {
@@ -579,27 +608,30 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
             vmax = max(vmax, sz[mb][r].y & 0x7fffu);
           }
         }
-        // ---- running maximum and sum; the value scales' power of two
-        float ref[2], keep[2];
+        // ---- running maximum, and the value scales' power of two.  Both stay as
+        // they are until a score passes the maximum by kSlack or a value scale its
+        // power of two, which is seldom behind the first tile.
+        if (__any_sync(0xffffffffu, tmax[0] > m[0] + kSlack || tmax[1] > m[1] + kSlack ||
+                                        vmax >= vlimit)) {
+          float keep[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float mt = fmaxf(m[j], max_over_rows(tmax[j]));
-          ref[j] = mt == -INFINITY ? 0.0f : mt;
-          keep[j] = exp2_(m[j] - ref[j]);
-          m[j] = mt;
-          l[j] *= keep[j];
-        }
-        // value scales below 2^e of the largest seen: p s' 2^(15 - e) < 2^15 keeps
-        // 11 bits for weights down to 2^-29 and none is lost above 2^-39
-        vmax = redux_max(vmax);
-        const int e = vmax == 0 ? -30 : vmax < 0x400u ? -14 : (int)(vmax >> 10) - 14;
-        if (e > ev) {
-          const float down = pow2f(ev - e);
-          keep[0] *= down;
-          keep[1] *= down;
-          ev = e;
-        }
-        if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+          for (int j = 0; j < 2; ++j) {
+            const float mt = fmaxf(m[j], max_over_rows(tmax[j]));
+            ref[j] = mt == -INFINITY ? 0.0f : mt;
+            keep[j] = exp2_(m[j] - ref[j]);
+            m[j] = mt;
+            l[j] *= keep[j];
+          }
+          // e: every value scale seen is below 2^e
+          vmax = redux_max(vmax);
+          const int e = vmax < 0x400u ? -14 : (int)(vmax >> 10) - 14;
+          if (e > ev) {
+            const float down = pow2f(ev - e);
+            keep[0] *= down;
+            keep[1] *= down;
+            ev = e;
+            vlimit = (uint32_t)(e + 15) << 10;
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -607,7 +639,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
           zs[0] *= keep[0];
           zs[1] *= keep[1];
         }
-        const float vup = pow2f(15 - ev);
+        // p s' 2^(15 - kSlack - e) < 2^15: 11 bits for weights down to 2^-23 of the
+        // maximum at the largest value scale, none lost above 2^-33
+        const float vup = pow2f(15 - kSlack - ev);
         uint32_t pf[MB][2];
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
@@ -652,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
       // ---- end of the unit in this CTA: values in real units
       float r[2][16];
       {
-        const float down = pow2f(ev - 15);
+        const float down = pow2f(ev - (15 - kSlack));
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           l[j] = sum_over_rows(l[j]);
@@ -740,15 +774,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
 }
 
 // Joins the partial sums of the units that more than one CTA worked on, in CTA
-// order, and writes zeros for the sequences without a visible token.  A CTA of
-// kJoinWarps warps takes one (sequence, query head): a lane holds 4 dimensions
+// order.  A CTA takes one (sequence, query head): a lane holds 4 dimensions
 // and the warps share the partial sums.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;                // at most
 template <int HB>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) {
   constexpr int TILE = Shape<HB>::kTile;
   __shared__ float part_m[kMaxCtas], part_l[kMaxCtas], red[kJoinWarps][128];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int64_t b = blockIdx.x;
   const int qh = blockIdx.y, group = P.q_heads / P.kv_heads;
   const int chunks = (group + kCols - 1) / kCols, kh = qh / group;
@@ -765,11 +798,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
   const Deal dl = deal(warp_sum(all) * subs, grid);
   const int64_t u0 = warp_sum(before) * subs + (int64_t)sub * tiles;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tiles == 0) {
-    if (threadIdx.x < 64)
-      reinterpret_cast<uint32_t*>(P.out)[(b * P.q_heads + qh) * 64 + threadIdx.x] = 0;
-    return;
-  }
+  if (tiles == 0) return;
   const int c0 = cta_of(dl, u0), n = cta_of(dl, u0 + tiles - 1) - c0 + 1;
   if (n == 1) return;
   // CTA c0 has its second slot for this unit unless it begins with it
@@ -779,7 +808,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
   auto slot = [&](int i) {
     return base + (i * 2 + (i == 0 ? second : 0)) * kWarps * kPartFloats;
   };
-  for (int i = threadIdx.x; i < n; i += 32 * kJoinWarps) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const float* s = slot(i);
     part_m[i] = s[kCols * 128 + col];
     part_l[i] = s[kCols * 128 + kCols + col];
@@ -791,7 +820,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
   const float ref = top == -INFINITY ? 0.0f : top;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-  for (int i = warp; i < n; i += kJoinWarps) {
+  for (int i = warp; i < n; i += warps) {
     const float f = exp2_(part_m[i] - ref);
     const float4 v = *reinterpret_cast<const float4*>(slot(i) + col * 128 + 4 * lane);
     acc.x = fmaf(f, v.x, acc.x);
@@ -812,8 +841,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kJoinWarps; ++k) sum += red[k][16 * g + i];
+      for (int k = 0; k < warps; ++k) sum += red[k][16 * g + i];
       v[i] = sum * inv;
     }
     store_result(P, v, b, qh, kh, (lane & 3) == 0);
@@ -836,7 +864,8 @@ cudaError_t launch(const AttnArgs& P, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)P.batch, (unsigned)P.q_heads);
-  cfg.blockDim = dim3(32 * kJoinWarps);
+  // few rows: more warps to each, they may have partial sums of every CTA
+  cfg.blockDim = dim3(P.batch * P.q_heads <= 2 * sms ? 32 * kJoinWarps : 128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

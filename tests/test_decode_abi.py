@@ -62,7 +62,7 @@ ATTN = dict(q=P, batch=2, qh=8, kh=2, ks=None, vs=None, kc=P, ksc=P, kz=P, vc=P,
     (dict(table=None), -1), (dict(ws=None), -1), (dict(ws_bytes=8), -1), (dict(kc=None), -1),
     (dict(vz=None), -1), (dict(ksc=None), -1), (dict(kh=0), -2), (dict(kh=3), -2),
     (dict(kh=129, qh=129), -2), (dict(qh=258, kh=2), -2), (dict(batch=65536), -2),
-    (dict(page=65537), -2), (dict(slots=1 << 40), -2), (dict(width=1 << 40), -2),
+    (dict(page=65537), -2), (dict(slots=1 << 31), -2), (dict(width=1 << 40), -2),
     (dict(width=1 << 39), -2), (dict(q=P + 8), -3), (dict(out=Q + 2), -3), (dict(ks=P + 8), -3),
     (dict(vs=P + 4), -3), (dict(kc=P + 8), -3), (dict(kz=P + 2), -3), (dict(vsc=P + 2), -3),
     (dict(ws=P + 8), -3), (dict(table=P + 2), -3), (dict(lens=P + 2), -3),
