@@ -184,14 +184,22 @@ __device__ __forceinline__ bool begin(const AttnArgs& P, int most, int subs, Wal
   return false;
 }
 
-// Cache row of visible token v, -1 where there is none.
-__device__ __forceinline__ int cache_row(const AttnArgs& P, const Walk& w, int v) {
-  if (v >= w.seq.vis) return -1;
+// Where visible token v lies: its page as the table has it (an asynchronous
+// load whose value is looked at one tile later) and its place in the page.
+struct Place {
+  int page, in;
+};
+__device__ __forceinline__ Place place(const AttnArgs& P, const Walk& w, int v) {
+  if (v >= w.seq.vis) return Place{-1, 0};
   const uint32_t pos = (uint32_t)(v < P.sinks ? v : v + w.seq.skip);
   const uint32_t page_in = pos / (uint32_t)P.page_size;
-  const int64_t page = __ldg(P.block_table + w.b * P.table_width + page_in);
-  const int64_t row = page * P.page_size + (pos - page_in * (uint32_t)P.page_size);
-  return page < 0 || row >= P.num_slots ? -1 : (int)row;
+  return Place{__ldg(P.block_table + w.b * P.table_width + page_in),
+               (int)(pos - page_in * (uint32_t)P.page_size)};
+}
+// Its cache row, -1 where there is none.
+__device__ __forceinline__ int cache_row(const AttnArgs& P, Place p) {
+  const int64_t row = (int64_t)p.page * P.page_size + p.in;
+  return p.page < 0 || row >= P.num_slots ? -1 : (int)row;
 }
 
 template <int HB>
@@ -201,18 +209,38 @@ struct Shape {
   static constexpr int kTile = kTok * kSplit;            // tokens a tile
   static constexpr int kRow = HB * 64 + 32;              // bytes a staged code row
   static constexpr int kCodes = kTile * kRow;            // keys or values of a tile
-  static constexpr int kScales = HB * kTile * 8;         // (sk, zk, sv, zv) halves
-  static constexpr int kStage = 2 * kCodes + kScales;
+  // per token and head the halves (sk, zk, sv, unused), then the value zero
+  // points in the order of the mma's operand, then a bit a token: not visible
+  static constexpr int kScales = HB * kTile * 8;
+  static constexpr int kZeros = HB * kTile * 2;
+  static constexpr int kMask = 16;
+  static constexpr int kStage = 2 * kCodes + kScales + kZeros + kMask;
   static constexpr int kStages = HB == 8 ? 3 : HB == 1 ? 3 : 2;
   // the warps of a head are joined two by two: one writes, one adds
   static constexpr int kJoin = kSplit > 1 ? kWarps / 2 * kPartFloats * 4 : 0;
   static constexpr size_t kSmem = kStages * kStage + kJoin + 2 * kStages * 8;
 };
 
-// 16 bytes, or zeros (and no read) for bytes = 0.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-               :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+// 16 bytes, both addresses with a constant offset.
+template <int OFFSET>
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;"
+               :: "r"(dst), "l"(src), "n"(OFFSET) : "memory");
+}
+template <int HB>
+__device__ __forceinline__ void copy_heads(uint32_t dst, const uint8_t* src) {
+  copy16<0>(dst, src);
+  if constexpr (HB > 1) copy16<64>(dst, src);
+  if constexpr (HB > 2) {
+    copy16<128>(dst, src);
+    copy16<192>(dst, src);
+  }
+  if constexpr (HB > 4) {
+    copy16<256>(dst, src);
+    copy16<320>(dst, src);
+    copy16<384>(dst, src);
+    copy16<448>(dst, src);
+  }
 }
 // Arrives (once a lane) when all of the lane's copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
@@ -350,39 +378,42 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
   };
 
   if (warp == kWarps) {
-    // ================= code rows, 16 bytes a lane
+    // ================= code rows: a lane copies 16 bytes of every head of a row,
+    // 4 lanes a row, so that the copies of a row differ by constants alone.  A
+    // token that is not visible gets the codes of row 0 (any codes do: its weight
+    // is zero).
     constexpr int N = TILE / 32;
-    constexpr int LANES = HB * 4;          // lanes a row
-    const uint32_t dst0 = smem_u32(smem) + lane / LANES * S::kRow + 16 * (lane % LANES);
+    const uint32_t dst0 = smem_u32(smem) + lane / 4 * S::kRow + 16 * (lane % 4);
     const int64_t pitch = (int64_t)P.kv_heads * 64;
-    int row[N];
-    auto rows = [&] {
+    Place at[N];
+    auto look = [&] {
 #pragma unroll
-      for (int j = 0; j < N; ++j) row[j] = cache_row(P, w, w.tile * TILE + j * 32 + lane);
+      for (int j = 0; j < N; ++j) at[j] = place(P, w, w.tile * TILE + j * 32 + lane);
     };
-    rows();
+    look();
     for (int64_t it = 0; it < count; ++it) {
       const int s = (int)(it % S::kStages);
-      const int64_t off0 = (int64_t)(w.sub / chunks) * HB * 64 + 16 * (lane % LANES);
+      const int64_t off0 = (int64_t)(w.sub / chunks) * HB * 64 + 16 * (lane % 4);
       const uint32_t dst = dst0 + s * S::kStage;
-      int now[N];
+      int row[N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) now[j] = row[j];
-      if (it + 1 < count) {                // the next tile's rows, while this one is copied
+      for (int j = 0; j < N; ++j) row[j] = max(cache_row(P, at[j]), 0);
+      if (it + 1 < count) {
         step(w);
-        rows();
+        look();
       }
       if (it >= S::kStages && !wait(&empty[s], (uint32_t)(it / S::kStages - 1) & 1)) break;
 #pragma unroll
       for (int j = 0; j < N; ++j)
-#pragma unroll 8
-        for (int i = 0; i < LANES; ++i) {
-          const int r = __shfl_sync(0xffffffffu, now[j], i * (32 / LANES) + lane / LANES);
-          const int64_t off = off0 + max(r, 0) * pitch;
-          const uint32_t to = dst + (uint32_t)(j * 32 + i * (32 / LANES)) * S::kRow;
-          const uint32_t bytes = r >= 0 ? 16 : 0;
-          copy16(to, P.k_codes + off, bytes);
-          copy16(to + S::kCodes, P.v_codes + off, bytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t off =
+              off0 + __shfl_sync(0xffffffffu, row[j], 8 * i + lane / 4) * pitch;
+          const uint8_t* kp = P.k_codes + off;
+          const uint8_t* vp = P.v_codes + off;
+          const uint32_t to = dst + (uint32_t)(j * 32 + 8 * i) * S::kRow;
+          copy_heads<HB>(to, kp);
+          copy_heads<HB>(to + S::kCodes, vp);
         }
       arrive_after_copies(&full[s]);
     }
@@ -396,17 +427,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
     };
     Loaded cur[N];
     const uint16_t* src[4] = {P.k_scales, P.k_zeros, P.v_scales, P.v_zeros};
-    int row[N];
+    Place at[N];
+    uint32_t hidden[N];
     int64_t head0;
-    auto rows = [&] {
+    auto look = [&] {
       head0 = (int64_t)(w.sub / chunks) * HB;
 #pragma unroll
-      for (int j = 0; j < N; ++j) row[j] = cache_row(P, w, w.tile * TILE + j * 32 + lane);
+      for (int j = 0; j < N; ++j) at[j] = place(P, w, w.tile * TILE + j * 32 + lane);
     };
     auto load = [&] {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const int r = row[j];
+        const int r = cache_row(P, at[j]);
+        hidden[j] = __ballot_sync(0xffffffffu, r < 0);
         const int64_t off = (int64_t)r * P.kv_heads + head0;
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
@@ -424,37 +457,46 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
               cur[j].v[a][0] = __ldg(src[a] + off);
             }
           } else {
-            // a token that is not visible: NaN in the key scale marks it, the
-            // rest is zero so that nothing of it reaches a sum
+            // not visible: zeros, so that nothing of it reaches a sum
 #pragma unroll
-            for (int h = 0; h < HB; ++h) cur[j].v[a][h] = a == 0 ? 0x7fff : 0;
+            for (int h = 0; h < HB; ++h) cur[j].v[a][h] = 0;
           }
         }
       }
     };
-    // the rows are looked up one tile further ahead than the scales are loaded
-    rows();
+    // the pages are looked up one tile further ahead than the scales are loaded
+    look();
     load();
     if (count > 1) {
       step(w);
-      rows();
+      look();
     }
+    // the lane's token in the mma's operand order: rows 2t and 2t + 1 of an
+    // accumulator are tokens t and 4 + (t + 2) % 4
+    const int r8 = lane & 7, zt = r8 < 4 ? r8 : (r8 + 2) & 3;
+    const int zpos = ((lane >> 4) * 4 + zt) * 4 + (lane >> 3 & 1) * 2 + (r8 >> 2);
     for (int64_t it = 0; it < count; ++it) {
       const int s = (int)(it % S::kStages);
       if (it >= S::kStages && !wait(&empty[s], (uint32_t)(it / S::kStages - 1) & 1)) break;
-      uint2* to = reinterpret_cast<uint2*>(smem + s * S::kStage + 2 * S::kCodes);
+      uint8_t* base = smem + s * S::kStage + 2 * S::kCodes;
+      uint2* to = reinterpret_cast<uint2*>(base);
+      uint16_t* zv = reinterpret_cast<uint16_t*>(base + S::kScales);
+      uint32_t* mask = reinterpret_cast<uint32_t*>(base + S::kScales + S::kZeros);
 #pragma unroll
-      for (int j = 0; j < N; ++j)
+      for (int j = 0; j < N; ++j) {
 #pragma unroll
-        for (int h = 0; h < HB; ++h)
+        for (int h = 0; h < HB; ++h) {
           to[h * TILE + j * 32 + lane] =
-              make_uint2(cur[j].v[0][h] | (uint32_t)cur[j].v[1][h] << 16,
-                         cur[j].v[2][h] | (uint32_t)cur[j].v[3][h] << 16);
+              make_uint2(cur[j].v[0][h] | (uint32_t)cur[j].v[1][h] << 16, cur[j].v[2][h]);
+          zv[h * TILE + j * 32 + zpos] = cur[j].v[3][h];
+        }
+        if (lane == 0) mask[j] = hidden[j];
+      }
       mbar_arrive(&full[s]);
       if (it + 1 < count) load();
       if (it + 2 < count) {
         step(w);
-        rows();
+        look();
       }
     }
   } else {
@@ -467,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
     const int mine = g & 1 ? 4 + (((g >> 1) + 2) & 3) : g >> 1;
     uint32_t qf[4][4];
     float fa[2], fz[2];                    // per column 2t, 2t + 1
-    float m[2], ref[2], l[2], zs[2], o[8][4];
+    float m[2], ref[2], l[2], zs[4], o[8][4];
     int ev = 0;
     uint32_t vlimit = 0;                   // fp16 bits of 2^ev
     int64_t it = 0;
@@ -557,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
           fa[j] = fj * 0x1p24f;
           fz[j] = fj * __shfl_sync(0xffffffffu, sum, (2 * t + j) * 4);
           m[j] = -INFINITY;
-          l[j] = zs[j] = 0.0f;
+          l[j] = zs[j] = zs[2 + j] = 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -576,6 +618,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
         const uint8_t* vb = kb + S::kCodes;
         const uint2* sb = reinterpret_cast<const uint2*>(smem + s * S::kStage + 2 * S::kCodes) +
                           hw * TILE + tok0;
+        const uint2* zb = reinterpret_cast<const uint2*>(smem + s * S::kStage + 2 * S::kCodes +
+                                                         S::kScales) +
+                          (hw * TILE + tok0) / 4 + t;
+        const uint32_t hidden =
+            *reinterpret_cast<const uint32_t*>(smem + s * S::kStage + 2 * S::kCodes + S::kScales +
+                                               S::kZeros + tok0 / 32 * 4) >> (tok0 % 32);
         float sc[MB][2][2];                // [block][row g or g + 8][column]
         uint2 sz[MB][2];
         float tmax[2] = {-INFINITY, -INFINITY};
@@ -601,13 +649,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
             const float2 k2 = half2_floats(sz[mb][r].x);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float a = k2.x * (fa[j] * c[2 * r + j] - k2.y * fz[j]);
-              sc[mb][r][j] = k2.x == k2.x ? a : -INFINITY;
-              tmax[j] = fmaxf(tmax[j], sc[mb][r][j]);
+              sc[mb][r][j] = k2.x * (fa[j] * c[2 * r + j] - k2.y * fz[j]);
             }
             vmax = max(vmax, sz[mb][r].y & 0x7fffu);
           }
         }
+        if (hidden != 0) {
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (hidden >> (mb * 16 + 8 * r + mine) & 1)
+                sc[mb][r][0] = sc[mb][r][1] = -INFINITY;
+        }
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            tmax[j] = fmax3(tmax[j], sc[mb][0][j], sc[mb][1][j]);
         // ---- running maximum, and the value scales' power of two.  Both stay as
         // they are until a score passes the maximum by kSlack or a value scale its
         // power of two, which is seldom behind the first tile.
@@ -636,8 +695,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
           for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[i][j] *= keep[j & 1];
-          zs[0] *= keep[0];
-          zs[1] *= keep[1];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) zs[j] *= keep[j & 1];
         }
         // p s' 2^(15 - kSlack - e) < 2^15: 11 bits for weights down to 2^-23 of the
         // maximum at the largest value scale, none lost above 2^-33
@@ -647,20 +706,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float2 v2 = half2_floats(sz[mb][r].y);
             const float p0 = exp2_(sc[mb][r][0] - ref[0]), p1 = exp2_(sc[mb][r][1] - ref[1]);
             l[0] += p0;
             l[1] += p1;
-            const float vs = v2.x * vup;
-            const uint32_t h = half2_bits(p0 * vs, p1 * vs);
-            const float2 rr = half2_floats(h);
-            zs[0] += rr.x * v2.y;
-            zs[1] += rr.y * v2.y;
-            pf[mb][r] = transpose8x8(h);
+            const float vs = f16_bits_to_f32((uint16_t)sz[mb][r].y) * vup;
+            pf[mb][r] = transpose8x8(half2_bits(p0 * vs, p1 * vs));
           }
         // ---- values
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
+          // the zero points as one more dimension (every row the same)
+          const uint2 z = zb[mb * 4];
+          mma16816(zs, z.x, z.x, z.y, z.y, pf[mb][0], pf[mb][1]);
           uint2 x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -690,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           l[j] = sum_over_rows(l[j]);
-          const float z = sum_over_rows(zs[j]);
+          const float z = zs[j];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             r[j][2 * i] = (o[i][j] * 0x1p24f - z) * down;
@@ -780,7 +837,8 @@ constexpr int kJoinWarps = 16;                // at most
 template <int HB>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) {
   constexpr int TILE = Shape<HB>::kTile;
-  __shared__ float part_m[kMaxCtas], part_l[kMaxCtas], red[kJoinWarps][128];
+  __shared__ float part_m[kMaxCtas], part_l[kMaxCtas];
+  __shared__ __align__(16) float red[kJoinWarps][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int64_t b = blockIdx.x;
   const int qh = blockIdx.y, group = P.q_heads / P.kv_heads;
@@ -830,6 +888,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
   }
   *reinterpret_cast<float4*>(&red[warp][4 * lane]) = acc;
   __syncthreads();
+  if (threadIdx.x < 128) {
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < warps; ++k) sum += red[k][threadIdx.x];
+    red[0][threadIdx.x] = sum;
+  }
+  __syncthreads();
   if (warp == 0) {
     float l = 0.0f;
     for (int i = lane; i < n; i += 32) l += part_l[i] * exp2_(part_m[i] - ref);
@@ -839,10 +904,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
     const int g = lane >> 2;
     float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float sum = 0.0f;
-      for (int k = 0; k < warps; ++k) sum += red[k][16 * g + i];
-      v[i] = sum * inv;
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = *reinterpret_cast<const float4*>(&red[0][16 * g + 4 * i]);
+      v[4 * i] = f.x * inv;
+      v[4 * i + 1] = f.y * inv;
+      v[4 * i + 2] = f.z * inv;
+      v[4 * i + 3] = f.w * inv;
     }
     store_result(P, v, b, qh, kh, (lane & 3) == 0);
   }
@@ -884,7 +951,9 @@ size_t attn_workspace_bytes(int64_t batch, int q_heads, int kv_heads) {
   return sizeof(float) * (size_t)at::kMaxCtas * 2 * at::kWarps * at::kPartFloats;
 }
 
-cudaError_t launch_attn_decode(const AttnArgs& P, cudaStream_t s) {
+cudaError_t launch_attn_decode(const AttnArgs& args, cudaStream_t s) {
+  AttnArgs P = args;
+  if (P.num_slots == 0) P.table_width = 0;    // no row to read: every sequence is empty
   // the widest block of heads whose rows and scales stay whole
   if (P.kv_heads % 8 == 0) return at::launch<8>(P, s);
   if (P.kv_heads % 4 == 0) return at::launch<4>(P, s);
