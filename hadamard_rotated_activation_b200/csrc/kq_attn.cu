@@ -227,19 +227,14 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
   asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;"
                :: "r"(dst), "l"(src), "n"(OFFSET) : "memory");
 }
+// Every 128th byte's 16 of a row of HB heads (64 bytes a head).
 template <int HB>
-__device__ __forceinline__ void copy_heads(uint32_t dst, const uint8_t* src) {
+__device__ __forceinline__ void copy_lines(uint32_t dst, const uint8_t* src) {
   copy16<0>(dst, src);
-  if constexpr (HB > 1) copy16<64>(dst, src);
-  if constexpr (HB > 2) {
-    copy16<128>(dst, src);
-    copy16<192>(dst, src);
-  }
+  if constexpr (HB > 2) copy16<128>(dst, src);
   if constexpr (HB > 4) {
     copy16<256>(dst, src);
-    copy16<320>(dst, src);
     copy16<384>(dst, src);
-    copy16<448>(dst, src);
   }
 }
 // Arrives (once a lane) when all of the lane's copies so far have landed.
@@ -378,12 +373,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
   };
 
   if (warp == kWarps) {
-    // ================= code rows: a lane copies 16 bytes of every head of a row,
-    // 4 lanes a row, so that the copies of a row differ by constants alone.  A
+    // ================= code rows: 8 lanes a row (4 when a row is one head), a lane
+    // 16 bytes of each of the row's 128-byte lines, so that the copies of a row
+    // differ by constants alone and every request is a whole line.  A
     // token that is not visible gets the codes of row 0 (any codes do: its weight
     // is zero).
     constexpr int N = TILE / 32;
-    const uint32_t dst0 = smem_u32(smem) + lane / 4 * S::kRow + 16 * (lane % 4);
+    constexpr int LANES = HB == 1 ? 4 : 8;
+    const uint32_t dst0 = smem_u32(smem) + lane / LANES * S::kRow + 16 * (lane % LANES);
     const int64_t pitch = (int64_t)P.kv_heads * 64;
     Place at[N];
     auto look = [&] {
@@ -393,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
     look();
     for (int64_t it = 0; it < count; ++it) {
       const int s = (int)(it % S::kStages);
-      const int64_t off0 = (int64_t)(w.sub / chunks) * HB * 64 + 16 * (lane % 4);
+      const int64_t off0 = (int64_t)(w.sub / chunks) * HB * 64 + 16 * (lane % LANES);
       const uint32_t dst = dst0 + s * S::kStage;
       int row[N];
 #pragma unroll
@@ -406,14 +403,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
 #pragma unroll
       for (int j = 0; j < N; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < LANES; ++i) {
+          constexpr int ROWS = 32 / LANES;
           const int64_t off =
-              off0 + __shfl_sync(0xffffffffu, row[j], 8 * i + lane / 4) * pitch;
-          const uint8_t* kp = P.k_codes + off;
-          const uint8_t* vp = P.v_codes + off;
-          const uint32_t to = dst + (uint32_t)(j * 32 + 8 * i) * S::kRow;
-          copy_heads<HB>(to, kp);
-          copy_heads<HB>(to + S::kCodes, vp);
+              off0 + __shfl_sync(0xffffffffu, row[j], ROWS * i + lane / LANES) * pitch;
+          const uint32_t to = dst + (uint32_t)(j * 32 + ROWS * i) * S::kRow;
+          copy_lines<HB>(to, P.k_codes + off);
+          copy_lines<HB>(to + S::kCodes, P.v_codes + off);
         }
       arrive_after_copies(&full[s]);
     }
