@@ -461,7 +461,7 @@ def kq_diag_tc_steps(a, b, d1, d2, status, stream=None, fp16=False) -> None:
 def kq_device_errors():
     """The six error words of the tensor-core kernel families (read and
     cleared): 4096-wide, 12288-wide, block-128 GEMM, fused inverse,
-    diagnostic, NVFP4 GEMM (bit 0) and decode attention (bit 8).  All zero: no bounded wait ran out since the last
+    diagnostic, NVFP4 GEMM.  All zero: no bounded wait ran out since the last
     call."""
     buf = (ctypes.c_uint * 6)()
     _check(lib().kq_device_errors(buf), "kq_device_errors")

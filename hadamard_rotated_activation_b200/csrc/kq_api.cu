@@ -461,9 +461,6 @@ KQ_API kq_status kq_device_errors(unsigned int* flags) {
   if (e == cudaSuccess) e = kq::take_tci_errors(&flags[3]);
   if (e == cudaSuccess) e = kq::take_diag_errors(&flags[4]);
   if (e == cudaSuccess) e = kq::take_gemm_errors(&flags[5]);
-  unsigned int attn = 0;
-  if (e == cudaSuccess) e = kq::take_attn_errors(&attn);
-  if (e == cudaSuccess) flags[5] |= attn << 8;
   return finish(e);
 }
 

@@ -7,11 +7,11 @@
 // Mathematics.  With codes u, scales s and zero points z of a token's head,
 //   a_t = f s_t (sum_d q_d u_td - z_t sum_d q_d),   p_t = 2^(a_t - max a)
 //   o_d = (sum_t (p_t s'_t) u_td - sum_t (p_t s'_t) z'_t) / sum_t p_t
-// so both products run on the bare 4-bit codes: a code masked out of its word
-// IS an fp16 number (u 2^-24, or 16 u 2^-24 for the upper nibble of a byte: an
-// fp16 bit pattern is linear up to 11 bits), exact on the tensor cores, and
-// costs 5 integer operations per 8 codes.  The factor 16 of the odd
-// dimensions is taken out of the query (keys) and the result (values).
+// so both products run on the bare 4-bit codes: bits masked out of their word
+// ARE an fp16 number (a pattern below 2^11 means itself times 2^-24), exact on
+// the tensor cores.  The operands are a byte, 16 h + l, and its low code l, which
+// cost 4 integer operations per 8 codes; h is taken out of them in the query's
+// coefficients (keys) and in the result (values).
 //
 // Bound by HBM: each visible token is read once, 68 bytes a head for the key
 // and 68 for the value.  mma.sync (m16n8k16) carries the contraction: its 16
@@ -27,13 +27,12 @@
 // partial sums in the workspace, which a second small kernel (launched as a
 // programmatic dependent) joins in CTA order.
 //
-// Per CTA: warp 8 copies the tiles' code rows into shared stages (16-byte
-// asynchronous copies: rows lie anywhere, and bulk copies issued lane by lane
-// cost 100 cycles each, 6500 a tile, which bounded the kernel), warp 9 their scales and zero points,
-// eight warps compute, each its own head (or its own part of the tokens when
-// there are fewer heads).  Stage rows are 32 bytes longer than a multiple of
-// 128, which makes both fragment reads free of bank conflicts.  Every wait is
-// bounded.
+// Per CTA: eight warps compute, each its own head (or its own part of the tokens
+// when there are fewer heads), and fill the shared stages together with 16-byte
+// asynchronous copies, one barrier a tile.  (Measured instead: bulk copies issued
+// lane by lane took 100 cycles each, 6500 a tile; extra warps for the copies
+// left the others 96 registers, which spilled.)  Stage rows are 32 bytes longer
+// than a multiple of 128, which keeps both fragment reads free of bank conflicts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,8 +46,8 @@ namespace at {
 
 using namespace sm100;
 
-constexpr int kWarps = 8;                     // compute warps
-constexpr int kThreads = 32 * (kWarps + 2);
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 // A running maximum is kept until a score passes it by more than this (in
 // powers of two); the weights stay below 2^kSlack.
 constexpr int kSlack = 6;
@@ -56,13 +55,6 @@ constexpr int kCols = 8;                      // query heads a unit carries
 constexpr int kMaxCtas = 320;
 constexpr int kMinTiles = 2;                  // tiles a CTA takes at least
 constexpr int kPartFloats = kCols * 128 + 2 * kCols;   // o, m, l of one head
-
-__device__ unsigned int g_attn_error = 0;
-
-// A warp waits together, and gives up together.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_attn_error));
-}
 
 // Tokens of one sequence: positions v < vis, v + skip from `sinks` on.
 struct Seq {
@@ -184,15 +176,24 @@ __device__ __forceinline__ bool begin(const AttnArgs& P, int most, int subs, Wal
   return false;
 }
 
+// pos / page_size for pos < 2^31 by a multiplication: with l = ceil(log2 d) and
+// M = ceil(2^(31 + l) / d), M d - 2^(31 + l) < d <= 2^l, so floor(pos M / 2^(31 + l))
+// is the quotient.  M = 0 stands for d = 1.
+struct PageDiv {
+  uint32_t mul, shift;
+};
+__device__ __forceinline__ uint32_t page_of(PageDiv d, uint32_t pos) {
+  return d.mul ? __umulhi(pos, d.mul) >> d.shift : pos;
+}
 // Where visible token v lies: its page as the table has it (an asynchronous
 // load whose value is looked at one tile later) and its place in the page.
 struct Place {
   int page, in;
 };
-__device__ __forceinline__ Place place(const AttnArgs& P, const Walk& w, int v) {
+__device__ __forceinline__ Place place(const AttnArgs& P, PageDiv d, const Walk& w, int v) {
   if (v >= w.seq.vis) return Place{-1, 0};
   const uint32_t pos = (uint32_t)(v < P.sinks ? v : v + w.seq.skip);
-  const uint32_t page_in = pos / (uint32_t)P.page_size;
+  const uint32_t page_in = page_of(d, pos);
   return Place{__ldg(P.block_table + w.b * P.table_width + page_in),
                (int)(pos - page_in * (uint32_t)P.page_size)};
 }
@@ -210,15 +211,18 @@ struct Shape {
   static constexpr int kRow = HB * 64 + 32;              // bytes a staged code row
   static constexpr int kCodes = kTile * kRow;            // keys or values of a tile
   // per token and head the halves (sk, zk, sv, unused), then the value zero
-  // points in the order of the mma's operand, then a bit a token: not visible
+  // points in the order of the mma's operand, then a byte a token: not visible
   static constexpr int kScales = HB * kTile * 8;
   static constexpr int kZeros = HB * kTile * 2;
-  static constexpr int kMask = 16;
+  static constexpr int kMask = kTile;
+  static constexpr int kLanes = HB == 1 ? 4 : 8;         // lanes that copy a row
+  static constexpr int kPass = 32 / kLanes;              // rows a warp copies at a time
+  static constexpr int kPasses = kTile / kWarps / kPass;
   static constexpr int kStage = 2 * kCodes + kScales + kZeros + kMask;
   static constexpr int kStages = HB == 8 ? 3 : HB == 1 ? 3 : 2;
   // the warps of a head are joined two by two: one writes, one adds
   static constexpr int kJoin = kSplit > 1 ? kWarps / 2 * kPartFloats * 4 : 0;
-  static constexpr size_t kSmem = kStages * kStage + kJoin + 2 * kStages * 8;
+  static constexpr size_t kSmem = kStages * kStage + kJoin;
 };
 
 // 16 bytes, both addresses with a constant offset.
@@ -237,10 +241,12 @@ __device__ __forceinline__ void copy_lines(uint32_t dst, const uint8_t* src) {
     copy16<384>(dst, src);
   }
 }
-// Arrives (once a lane) when all of the lane's copies so far have landed.
-__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void commit_copies() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {   // at most N groups still under way
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -328,38 +334,25 @@ __device__ __forceinline__ void store_result(const AttnArgs& P, float (&v)[16], 
 }
 
 template <int HB>
-__global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
+__global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages) {
   using S = Shape<HB>;
   constexpr int TILE = S::kTile, MB = S::kTok / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   float* join = reinterpret_cast<float*>(smem + S::kStages * S::kStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStage + S::kJoin);
-  uint64_t* empty = full + S::kStages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&full[s], 64);
-      mbar_init(&empty[s], kWarps);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncthreads();
-
   const int most = longest(P);
   const int group = P.q_heads / P.kv_heads, chunks = (group + kCols - 1) / kCols;
   const int subs = P.kv_heads / HB * chunks;
   Walk w;
   int64_t count = 0;
   const bool any = begin<TILE>(P, most, subs, w, count);
-  if (warp == kWarps + 1) {
-    // sequences without a visible token have no tile: their rows are zeros
-    for (int64_t b = blockIdx.x; b < P.batch; b += gridDim.x)
-      if (sequence(P, most, b).vis == 0)
-        for (int i = lane; i < P.q_heads * 16; i += 32)
-          reinterpret_cast<uint4*>(P.out)[b * P.q_heads * 16 + i] = make_uint4(0, 0, 0, 0);
-  }
+  // sequences without a visible token have no tile: their rows are zeros
+  for (int64_t b = blockIdx.x; b < P.batch; b += gridDim.x)
+    if (sequence(P, most, b).vis == 0)
+      for (int i = threadIdx.x; i < P.q_heads * 16; i += kThreads)
+        reinterpret_cast<uint4*>(P.out)[b * P.q_heads * 16 + i] = make_uint4(0, 0, 0, 0);
   if (!any) return;
 
   auto step = [&](Walk& x) {
@@ -372,130 +365,96 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
     }
   };
 
-  if (warp == kWarps) {
-    // ================= code rows: 8 lanes a row (4 when a row is one head), a lane
-    // 16 bytes of each of the row's 128-byte lines, so that the copies of a row
-    // differ by constants alone and every request is a whole line.  A
-    // token that is not visible gets the codes of row 0 (any codes do: its weight
-    // is zero).
-    constexpr int N = TILE / 32;
-    constexpr int LANES = HB == 1 ? 4 : 8;
-    const uint32_t dst0 = smem_u32(smem) + lane / LANES * S::kRow + 16 * (lane % LANES);
-    const int64_t pitch = (int64_t)P.kv_heads * 64;
-    Place at[N];
-    auto look = [&] {
+  // ================= filling the stages.  A warp copies kTile / 8 rows, 8 lanes a
+  // row (4 when a row is one head), a lane 16 bytes of each of the row's 128-byte
+  // lines: the copies of a row differ by constants alone, and every request is a
+  // whole line.  A token that is not visible gets the codes of row 0 (any codes
+  // do: its weight is zero).  The first four lanes of a row also load its scales
+  // and zero points, an array each, which go through registers into the stage one
+  // tile later.  Pages are looked up one tile ahead.
+  const int arr = lane % S::kLanes;
+  const uint16_t* sc_from = arr == 0 ? P.k_scales : arr == 1 ? P.k_zeros
+                            : arr == 2 ? P.v_scales : P.v_zeros;
+  const int my_row = warp * (TILE / kWarps) + lane / S::kLanes;    // + pass * kPass
+  Walk ahead = w;
+  int64_t fetched = 0;                    // tiles whose copies were issued
+  int fill = 0, late = -1;                // stage to fill; stage whose scales are still in registers
+  Place at[S::kPasses];
+  uint16_t sreg[S::kPasses][HB];
+  bool gone[S::kPasses];
+  auto look = [&] {
 #pragma unroll
-      for (int j = 0; j < N; ++j) at[j] = place(P, w, w.tile * TILE + j * 32 + lane);
-    };
-    look();
-    for (int64_t it = 0; it < count; ++it) {
-      const int s = (int)(it % S::kStages);
-      const int64_t off0 = (int64_t)(w.sub / chunks) * HB * 64 + 16 * (lane % LANES);
-      const uint32_t dst = dst0 + s * S::kStage;
-      int row[N];
+    for (int j = 0; j < S::kPasses; ++j)
+      at[j] = place(P, pages, ahead, ahead.tile * TILE + my_row + j * S::kPass);
+  };
+  auto store_scales = [&] {
+    if (late < 0) return;
+    uint8_t* base = smem + late * S::kStage + 2 * S::kCodes;
 #pragma unroll
-      for (int j = 0; j < N; ++j) row[j] = max(cache_row(P, at[j]), 0);
-      if (it + 1 < count) {
-        step(w);
-        look();
+    for (int j = 0; j < S::kPasses; ++j) {
+      const int tok = my_row + j * S::kPass, r16 = tok & 15, r8 = tok & 7;
+      // the mma's operand order: rows 2t and 2t + 1 of an accumulator are tokens t
+      // and 4 + (t + 2) % 4
+      const int zt = r8 < 4 ? r8 : (r8 + 2) & 3;
+      const int zpos = (tok >> 4) * 16 + zt * 4 + (r16 >> 3) * 2 + (r8 >> 2);
+      uint16_t* to = arr < 3 ? reinterpret_cast<uint16_t*>(base) + tok * 4 + arr
+                             : reinterpret_cast<uint16_t*>(base + S::kScales) + zpos;
+      const int pitch = arr < 3 ? TILE * 4 : TILE;
+      if (arr < 4) {
+#pragma unroll
+        for (int h = 0; h < HB; ++h) to[h * pitch] = sreg[j][h];
       }
-      if (it >= S::kStages && !wait(&empty[s], (uint32_t)(it / S::kStages - 1) & 1)) break;
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-#pragma unroll
-        for (int i = 0; i < LANES; ++i) {
-          constexpr int ROWS = 32 / LANES;
-          const int64_t off =
-              off0 + __shfl_sync(0xffffffffu, row[j], ROWS * i + lane / LANES) * pitch;
-          const uint32_t to = dst + (uint32_t)(j * 32 + ROWS * i) * S::kRow;
-          copy_lines<HB>(to, P.k_codes + off);
-          copy_lines<HB>(to + S::kCodes, P.v_codes + off);
-        }
-      arrive_after_copies(&full[s]);
+      if (arr == 0) base[S::kScales + S::kZeros + tok] = gone[j];
     }
-    // no copy may still be in flight when the CTA exits
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == kWarps + 1) {
-    // ================= scales and zero points: (sk, zk, sv, zv) a token and head
-    constexpr int N = TILE / 32;
-    struct Loaded {
-      uint16_t v[4][HB];
-    };
-    Loaded cur[N];
-    const uint16_t* src[4] = {P.k_scales, P.k_zeros, P.v_scales, P.v_zeros};
-    Place at[N];
-    uint32_t hidden[N];
-    int64_t head0;
-    auto look = [&] {
-      head0 = (int64_t)(w.sub / chunks) * HB;
+    late = -1;
+  };
+  auto fetch = [&] {
+    if (fetched < count) {
+      const int64_t head0 = (int64_t)(ahead.sub / chunks) * HB;
 #pragma unroll
-      for (int j = 0; j < N; ++j) at[j] = place(P, w, w.tile * TILE + j * 32 + lane);
-    };
-    auto load = [&] {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
+      for (int j = 0; j < S::kPasses; ++j) {
         const int r = cache_row(P, at[j]);
-        hidden[j] = __ballot_sync(0xffffffffu, r < 0);
-        const int64_t off = (int64_t)r * P.kv_heads + head0;
+        const int64_t row = (int64_t)max(r, 0) * P.kv_heads + head0;
+        const int64_t off = row * 64 + 16 * arr;
+        const uint32_t to = smem_u32(smem) + fill * S::kStage +
+                            (uint32_t)(my_row + j * S::kPass) * S::kRow + 16 * arr;
+        copy_lines<HB>(to, P.k_codes + off);
+        copy_lines<HB>(to + S::kCodes, P.v_codes + off);
+        gone[j] = r < 0;
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          if (r >= 0) {
-            if constexpr (HB == 8) {
-              *reinterpret_cast<uint4*>(cur[j].v[a]) =
-                  __ldg(reinterpret_cast<const uint4*>(src[a] + off));
-            } else if constexpr (HB == 4) {
-              *reinterpret_cast<uint2*>(cur[j].v[a]) =
-                  __ldg(reinterpret_cast<const uint2*>(src[a] + off));
-            } else if constexpr (HB == 2) {
-              *reinterpret_cast<uint32_t*>(cur[j].v[a]) =
-                  __ldg(reinterpret_cast<const uint32_t*>(src[a] + off));
-            } else {
-              cur[j].v[a][0] = __ldg(src[a] + off);
-            }
-          } else {
-            // not visible: zeros, so that nothing of it reaches a sum
-#pragma unroll
-            for (int h = 0; h < HB; ++h) cur[j].v[a][h] = 0;
-          }
+        for (int h = 0; h < HB; ++h) sreg[j][h] = 0;
+        if (r >= 0 && arr < 4) {
+          if constexpr (HB == 8)
+            *reinterpret_cast<uint4*>(sreg[j]) = __ldg(reinterpret_cast<const uint4*>(sc_from + row));
+          else if constexpr (HB == 4)
+            *reinterpret_cast<uint2*>(sreg[j]) = __ldg(reinterpret_cast<const uint2*>(sc_from + row));
+          else if constexpr (HB == 2)
+            *reinterpret_cast<uint32_t*>(sreg[j]) =
+                __ldg(reinterpret_cast<const uint32_t*>(sc_from + row));
+          else
+            sreg[j][0] = __ldg(sc_from + row);
         }
       }
-    };
-    // the pages are looked up one tile further ahead than the scales are loaded
-    look();
-    load();
-    if (count > 1) {
-      step(w);
-      look();
-    }
-    // the lane's token in the mma's operand order: rows 2t and 2t + 1 of an
-    // accumulator are tokens t and 4 + (t + 2) % 4
-    const int r8 = lane & 7, zt = r8 < 4 ? r8 : (r8 + 2) & 3;
-    const int zpos = ((lane >> 4) * 4 + zt) * 4 + (lane >> 3 & 1) * 2 + (r8 >> 2);
-    for (int64_t it = 0; it < count; ++it) {
-      const int s = (int)(it % S::kStages);
-      if (it >= S::kStages && !wait(&empty[s], (uint32_t)(it / S::kStages - 1) & 1)) break;
-      uint8_t* base = smem + s * S::kStage + 2 * S::kCodes;
-      uint2* to = reinterpret_cast<uint2*>(base);
-      uint16_t* zv = reinterpret_cast<uint16_t*>(base + S::kScales);
-      uint32_t* mask = reinterpret_cast<uint32_t*>(base + S::kScales + S::kZeros);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-#pragma unroll
-        for (int h = 0; h < HB; ++h) {
-          to[h * TILE + j * 32 + lane] =
-              make_uint2(cur[j].v[0][h] | (uint32_t)cur[j].v[1][h] << 16, cur[j].v[2][h]);
-          zv[h * TILE + j * 32 + zpos] = cur[j].v[3][h];
-        }
-        if (lane == 0) mask[j] = hidden[j];
-      }
-      mbar_arrive(&full[s]);
-      if (it + 1 < count) load();
-      if (it + 2 < count) {
-        step(w);
+      late = fill;
+      if (++fill == S::kStages) fill = 0;
+      if (++fetched < count) {
+        step(ahead);
         look();
       }
     }
-  } else {
+    commit_copies();
+  };
+  look();
+#pragma unroll 1
+  for (int i = 0; i + 1 < S::kStages; ++i) {
+
+
+    store_scales();
+    fetch();
+  }
+
+  int stage = 0;
+  {
     // ================= compute: head `hw` of the block, tokens tok0 .. of a tile
     const int hw = warp / S::kSplit, part = warp % S::kSplit;
     const int tok0 = part * S::kTok;
@@ -507,10 +466,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
     float fa[2], fz[2];                    // per column 2t, 2t + 1
     float m[2], ref[2], l[2], zs[4], o[8][4];
     int ev = 0;
-    uint32_t vlimit = 0;                   // fp16 bits of 2^ev
+    bool fresh = false;                    // no tile of the unit seen yet
     int64_t it = 0;
     int segment = 0;
-    bool ok = true;                        // false: a wait ran out, nothing more is stored
     while (it < count) {
       // ---- the unit's query, rotated; lane (g, t) holds dimensions 32 t .. of column g
       const int kh = w.sub / chunks * HB + hw;
@@ -571,20 +529,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // fp16 with a power of two per column that puts its largest element in
-        // [2^14, 2^15): 11 significant bits over 28 binades
+        // [2^13, 2^14): 11 significant bits over 27 binades
         const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-        const int sh = top > 0.0f ? min(max(14 - ex, -120), 120) : 0;
+        const int sh = top > 0.0f ? min(max(13 - ex, -120), 120) : 0;
         const float up = pow2f(sh);
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float lo = q[8 * i + j] * up, hi = q[8 * i + 4 + j] * up;
-            qf[i][j] = half2_bits(lo, hi);
+            // a byte 16 h + l times q_odd / 16, its low code l times the rest of
+            // q_even; the sum is that of the coefficients as rounded
+            const int k = j & 2;
+            float lo = q[8 * i + k + 1] * 0.0625f, hi = q[8 * i + 4 + k + 1] * 0.0625f;
+            if (!(j & 1)) {
+              lo = q[8 * i + k] - lo;
+              hi = q[8 * i + 4 + k] - hi;
+            }
+            qf[i][j] = half2_bits(lo * up, hi * up);
             const float2 r = half2_floats(qf[i][j]);
-            sum += r.x + r.y;
-            if (j & 1) qf[i][j] = half2_bits(r.x * 0.0625f, r.y * 0.0625f);
+            sum += (r.x + r.y) * (j & 1 ? 17.0f : 1.0f);
           }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -595,21 +559,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
           fa[j] = fj * 0x1p24f;
           fz[j] = fj * __shfl_sync(0xffffffffu, sum, (2 * t + j) * 4);
           m[j] = -INFINITY;
+          ref[j] = 0.0f;
           l[j] = zs[j] = zs[2 + j] = 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-        ref[0] = ref[1] = 0.0f;
         ev = -14;
-        vlimit = 0x400u;
+        fresh = true;
       }
       const int64_t todo = min((int64_t)(w.tiles - w.tile), count - it);
       for (int64_t end = it + todo; it < end; ++it) {
-        const int s = (int)(it % S::kStages);
-        ok = ok && wait(&full[s], (uint32_t)(it / S::kStages) & 1);
-        if (!ok) continue;
+        // the tile's copies have landed and its scales are stored, and every warp
+        // is done with the stage that is filled next
+        wait_copies<S::kStages - 2>();
+        store_scales();
+        __syncthreads();
+        fetch();
+        const int s = stage;
+        if (++stage == S::kStages) stage = 0;
         const uint8_t* kb = smem + s * S::kStage + tok0 * S::kRow + hw * 64;
         const uint8_t* vb = kb + S::kCodes;
         const uint2* sb = reinterpret_cast<const uint2*>(smem + s * S::kStage + 2 * S::kCodes) +
@@ -617,13 +586,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
         const uint2* zb = reinterpret_cast<const uint2*>(smem + s * S::kStage + 2 * S::kCodes +
                                                          S::kScales) +
                           (hw * TILE + tok0) / 4 + t;
-        const uint32_t hidden =
-            *reinterpret_cast<const uint32_t*>(smem + s * S::kStage + 2 * S::kCodes + S::kScales +
-                                               S::kZeros + tok0 / 32 * 4) >> (tok0 % 32);
-        float sc[MB][2][2];                // [block][row g or g + 8][column]
-        uint2 sz[MB][2];
-        float tmax[2] = {-INFINITY, -INFINITY};
-        uint32_t vmax = 0;
+        const uint32_t hidden = __ballot_sync(
+            0xffffffffu, smem[s * S::kStage + 2 * S::kCodes + S::kScales + S::kZeros + tok0 +
+                              lane % S::kTok]);
+        float sc[MB][2][2];                // [block][row g or g + 8][column], minus ref
+        float vs[MB][2];                   // value scale of the row, times 2^(15 - kSlack - ev)
+        const float vup = pow2f(15 - kSlack - ev);
+        float vtop = 0.0f;
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
           const uint4 ka = *reinterpret_cast<const uint4*>(kb + (mb * 16 + mine) * S::kRow + t * 16);
@@ -633,22 +602,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
           float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            mma16816(c, xa[i] & 0x000f000fu, xc[i] & 0x000f000fu, xa[i] & 0x00f000f0u,
-                     xc[i] & 0x00f000f0u, qf[i][0], qf[i][1]);
-            const uint32_t ya = xa[i] >> 8, yc = xc[i] >> 8;
-            mma16816(c, ya & 0x000f000fu, yc & 0x000f000fu, ya & 0x00f000f0u, yc & 0x00f000f0u,
-                     qf[i][2], qf[i][3]);
+            mma16816(c, xa[i] & 0x000f000fu, xc[i] & 0x000f000fu, xa[i] & 0x00ff00ffu,
+                     xc[i] & 0x00ff00ffu, qf[i][0], qf[i][1]);
+            const uint32_t ya = __byte_perm(xa[i], 0, 0x4341), yc = __byte_perm(xc[i], 0, 0x4341);
+            mma16816(c, ya & 0x000f000fu, yc & 0x000f000fu, ya, yc, qf[i][2], qf[i][3]);
           }
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            sz[mb][r] = sb[mb * 16 + 8 * r + mine];
-            const float2 k2 = half2_floats(sz[mb][r].x);
+            const uint2 sz = sb[mb * 16 + 8 * r + mine];
+            const float2 k2 = half2_floats(sz.x);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              sc[mb][r][j] = k2.x * (fa[j] * c[2 * r + j] - k2.y * fz[j]);
-            }
-            vmax = max(vmax, sz[mb][r].y & 0x7fffu);
+            for (int j = 0; j < 2; ++j)
+              sc[mb][r][j] = fmaf(k2.x, fmaf(fa[j], c[2 * r + j], -k2.y * fz[j]), -ref[j]);
+            vs[mb][r] = f16_bits_to_f32((uint16_t)sz.y) * vup;
           }
+          vtop = fmax3(vtop, fabsf(vs[mb][0]), fabsf(vs[mb][1]));
         }
         if (hidden != 0) {
 #pragma unroll
@@ -658,35 +626,42 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
               if (hidden >> (mb * 16 + 8 * r + mine) & 1)
                 sc[mb][r][0] = sc[mb][r][1] = -INFINITY;
         }
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            tmax[j] = fmax3(tmax[j], sc[mb][0][j], sc[mb][1][j]);
         // ---- running maximum, and the value scales' power of two.  Both stay as
         // they are until a score passes the maximum by kSlack or a value scale its
         // power of two, which is seldom behind the first tile.
-        if (__any_sync(0xffffffffu, tmax[0] > m[0] + kSlack || tmax[1] > m[1] + kSlack ||
-                                        vmax >= vlimit)) {
+        float stop[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) stop[j] = fmax3(stop[j], sc[mb][0][j], sc[mb][1][j]);
+        if (fresh || __any_sync(0xffffffffu, fmaxf(stop[0], stop[1]) > (float)kSlack ||
+                                                 vtop > (float)(1 << (15 - kSlack)))) {
+          fresh = false;
           float keep[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float mt = fmaxf(m[j], max_over_rows(tmax[j]));
-            ref[j] = mt == -INFINITY ? 0.0f : mt;
-            keep[j] = exp2_(m[j] - ref[j]);
-            m[j] = mt;
+            const float mt = fmaxf(m[j], max_over_rows(stop[j]) + ref[j]);
+            const float next = mt == -INFINITY ? 0.0f : mt;
+            keep[j] = exp2_(m[j] - next);
             l[j] *= keep[j];
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) sc[mb][r][j] += ref[j] - next;
+            m[j] = mt;
+            ref[j] = next;
           }
-          // e: every value scale seen is below 2^e
-          vmax = redux_max(vmax);
-          const int e = vmax < 0x400u ? -14 : (int)(vmax >> 10) - 14;
-          if (e > ev) {
-            const float down = pow2f(ev - e);
-            keep[0] *= down;
-            keep[1] *= down;
-            ev = e;
-            vlimit = (uint32_t)(e + 15) << 10;
-          }
+          // every value scale seen is below 2^ev
+          const uint32_t bits = redux_max(__float_as_uint(vtop));
+          const int up = max((int)(bits >> 23) - 126 - (15 - kSlack), 0);
+          const float down = pow2f(-up);
+          ev += up;
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) vs[mb][r] *= down;
+          keep[0] *= down;
+          keep[1] *= down;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -694,19 +669,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) zs[j] *= keep[j & 1];
         }
-        // p s' 2^(15 - kSlack - e) < 2^15: 11 bits for weights down to 2^-23 of the
+        // p s' 2^(15 - kSlack - ev) < 2^15: 11 bits for weights down to 2^-23 of the
         // maximum at the largest value scale, none lost above 2^-33
-        const float vup = pow2f(15 - kSlack - ev);
         uint32_t pf[MB][2];
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float p0 = exp2_(sc[mb][r][0] - ref[0]), p1 = exp2_(sc[mb][r][1] - ref[1]);
+            const float p0 = exp2_(sc[mb][r][0]), p1 = exp2_(sc[mb][r][1]);
             l[0] += p0;
             l[1] += p1;
-            const float vs = f16_bits_to_f32((uint16_t)sz[mb][r].y) * vup;
-            pf[mb][r] = transpose8x8(half2_bits(p0 * vs, p1 * vs));
+            pf[mb][r] = transpose8x8(half2_bits(p0 * vs[mb][r], p1 * vs[mb][r]));
           }
         // ---- values
 #pragma unroll
@@ -726,15 +699,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
                                        : __byte_perm(x[0].y, x[1].y, sel);
             const uint32_t y23 = j < 2 ? __byte_perm(x[2].x, x[3].x, sel)
                                        : __byte_perm(x[2].y, x[3].y, sel);
-            mma16816(o[2 * j], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
-                     y23 & 0x00f000f0u, pf[mb][0], pf[mb][1]);
-            const uint32_t h01 = y01 >> 8, h23 = y23 >> 8;
-            mma16816(o[2 * j + 1], h01 & 0x000f000fu, h01 & 0x00f000f0u, h23 & 0x000f000fu,
-                     h23 & 0x00f000f0u, pf[mb][0], pf[mb][1]);
+            mma16816(o[2 * j], y01 & 0x000f000fu, y01 & 0x00ff00ffu, y23 & 0x000f000fu,
+                     y23 & 0x00ff00ffu, pf[mb][0], pf[mb][1]);
+            const uint32_t h01 = __byte_perm(y01, 0, 0x4341), h23 = __byte_perm(y23, 0, 0x4341);
+            mma16816(o[2 * j + 1], h01 & 0x000f000fu, h01, h23 & 0x000f000fu, h23, pf[mb][0],
+                     pf[mb][1]);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
       }
       // ---- end of the unit in this CTA: values in real units
       float r[2][16];
@@ -747,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             r[j][2 * i] = (o[i][j] * 0x1p24f - z) * down;
-            r[j][2 * i + 1] = (o[i][2 + j] * 0x1p20f - z) * down;
+            r[j][2 * i + 1] = ((o[i][2 + j] - o[i][j]) * 0x1p20f - z) * down;
           }
         }
       }
@@ -767,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
               slot[kCols * 128 + kCols + 2 * t + j] = l[j];
             }
           }
-          asm volatile("bar.sync 1, %0;" :: "n"(32 * kWarps) : "memory");
+          __syncthreads();
           if (part < half) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -787,11 +758,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P) {
               m[j] = mt;
             }
           }
-          asm volatile("bar.sync 1, %0;" :: "n"(32 * kWarps) : "memory");
+          __syncthreads();
         }
       }
       const bool whole = todo == w.tiles;
-      if (part == 0 && ok) {
+      if (part == 0) {
         if (whole) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -922,7 +893,14 @@ cudaError_t launch(const AttnArgs& P, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-  k_attn<HB><<<grid, kThreads, Shape<HB>::kSmem, s>>>(P);
+  PageDiv d{0, 0};
+  if (P.page_size > 1) {
+    uint32_t l = 1;
+    while ((1u << l) < (uint32_t)P.page_size) ++l;
+    d.mul = (uint32_t)(((uint64_t(1) << (31 + l)) + P.page_size - 1) / P.page_size);
+    d.shift = l - 1;
+  }
+  k_attn<HB><<<grid, kThreads, Shape<HB>::kSmem, s>>>(P, d);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -955,14 +933,6 @@ cudaError_t launch_attn_decode(const AttnArgs& args, cudaStream_t s) {
   if (P.kv_heads % 4 == 0) return at::launch<4>(P, s);
   if (P.kv_heads % 2 == 0) return at::launch<2>(P, s);
   return at::launch<1>(P, s);
-}
-
-// Reads and clears the error word of the attention kernel (device-synchronous).
-cudaError_t take_attn_errors(unsigned int* out) {
-  const unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, at::g_attn_error, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(at::g_attn_error, &zero, sizeof(unsigned int));
 }
 
 }  // namespace kq

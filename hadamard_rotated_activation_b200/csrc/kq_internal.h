@@ -72,7 +72,6 @@ struct AttnArgs {
 };
 size_t attn_workspace_bytes(int64_t batch, int q_heads, int kv_heads);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
-cudaError_t take_attn_errors(unsigned int* out);
 
 // Pages of a paged INT4 cache copied to other pages (kq_kvcopy.cu).
 cudaError_t launch_kv_copy(const int32_t* pairs, int64_t n_pairs, int page_size,

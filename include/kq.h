@@ -413,8 +413,7 @@ KQ_API kq_status kq_kv_copy_pages(const int32_t* pairs, int64_t n_pairs, int pag
  * provisional scale; bit 2: a fix-up warp waited too long), [1] the
  * 12288-wide kernel, [2] the block-128 GEMM kernel, [3] the fused dequant +
  * inverse kernel, [4] kq_diag_wait_timeout (bit 0), [5] the NVFP4 GEMM
- * (bit 0, since ABI version 1.1; 1.0 had 5 words) and the decode attention (bit 8,
- * since 1.2).  All zero: no failure
+ * (since ABI version 1.1; 1.0 had 5 words).  All zero: no failure
  * since the last call.  The read synchronizes the device.  The pages have no
  * counterpart to this entry point.
  */
