@@ -65,7 +65,8 @@ struct Params {
   int tiles;                              // 16-row tiles of a cluster
   int seg;                                // groups whose x is staged at a time
   int parts;                              // batches of a CTA: sums kept apart
-  int ranks;                              // CTAs of a cluster, which split k
+  int ranks, rank_shift;                  // CTAs of a cluster, which split k: 2^rank_shift
+  int wide;                               // scales of kBatch groups in one load
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -124,6 +125,17 @@ __device__ __forceinline__ Eight load8(const Params& P, int tok, int k0) {
     if (!P.x_bf16) e.b = __ldg(p + 1);
   }
   return e;
+}
+
+// Zeros in the columns behind the last one (once; nothing else writes them).
+template <int NT>
+__device__ __forceinline__ void clear_columns(const Params& P, int cols, uint4* xs, float2* xf) {
+  constexpr int kThreads = Shape<NT>::kThreads;
+  if (cols == 8 * NT) return;
+  for (int i = threadIdx.x; i < P.seg * NT * 128; i += kThreads)
+    if ((i >> 2 & 7) + 8 * (i >> 7 & (NT - 1)) >= cols) xs[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < P.seg * NT * 8; i += kThreads)
+    if ((i & (8 * NT - 1)) >= cols) xf[i] = make_float2(0.0f, 0.0f);
 }
 
 // Stages x of groups [g0, g0 + ng) for the columns of NT mma tiles.  16 lanes take
@@ -202,12 +214,17 @@ __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, uint4* 
               make_uint4(h[0], h[1], h[2], h[3]);
           // the sum of the group (of both parts at once) rides on the first column
           if (lane16 == 0)
-            xf[gi * NT * 8 + col] = part == 0 ? make_float2(pow2f(-sh), sum)
+            xf[gi * NT * 8 + col] = part == 0 ? make_float2(pow2f(-sh), sum * 0x1p-24f)
                                               : make_float2(pow2f(-sh) * 0x1p-11f, 0.0f);
         }
       }
     }
   }
+}
+
+// First group of a rank (ranks is a power of two).
+__device__ __forceinline__ int rank_begin(const Params& P, int rank) {
+  return (int)((uint32_t)(rank * P.groups) >> P.rank_shift);
 }
 
 // A unit of work as loaded: 16 rows (g and g + 8 of a lane) by kBatch groups.
@@ -232,6 +249,31 @@ __device__ __forceinline__ void load_unit(const Params& P, int64_t row0, int g0,
       u.a[i] = load_codes(ca + i * 64);
       u.b[i] = load_codes(cb + i * 64);
     }
+  }
+  if (P.wide && FMT == KQ_FMT_INT4_ASYM) {
+    const uint16_t* s16 = static_cast<const uint16_t*>(P.scales) + g0;
+    const uint16_t* z16 = P.zeros + g0;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int64_t at = (r ? rb : ra) * P.groups;
+      uint32_t* to = r ? u.sb : u.sa;
+      uint32_t sw[kBatch / 2], zw[kBatch / 2];
+      if constexpr (kBatch == 4) {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(s16 + at));
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(z16 + at));
+        sw[0] = a.x;
+        sw[1] = a.y;
+        zw[0] = b.x;
+        zw[1] = b.y;
+      } else {
+        sw[0] = __ldg(reinterpret_cast<const uint32_t*>(s16 + at));
+        zw[0] = __ldg(reinterpret_cast<const uint32_t*>(z16 + at));
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        to[i] = __byte_perm(sw[i / 2], zw[i / 2], i & 1 ? 0x7632 : 0x5410);
+    }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < kBatch; ++i) {
@@ -258,7 +300,7 @@ __device__ __forceinline__ void load_unit(const Params& P, int64_t row0, int g0,
 
 template <int FMT, int NT, int kBatch>
 __device__ __forceinline__ void compute_unit(const Params& P, const Unit<FMT, kBatch>& u, int gl0, int ng,
-                                             int cols, const uint4* xs, const float2* xf,
+                                             const uint4* xs, const float2* xf,
                                              float (&acc)[NT][4]) {
   constexpr bool INT4 = FMT == KQ_FMT_INT4_SYM || FMT == KQ_FMT_INT4_ASYM;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -304,16 +346,16 @@ __device__ __forceinline__ void compute_unit(const Params& P, const Unit<FMT, kB
     for (int j = 0; j < 4; ++j) {
       uint32_t fa[4], fb[4];
       if (INT4) {
-        const uint32_t flip = FMT == KQ_FMT_INT4_SYM ? 0x88888888u : 0u;
-        const uint32_t va = xa[j] ^ flip, vb = xb[j] ^ flip;
-        fa[0] = va & 0x000f000fu;
-        fa[1] = va & 0x00f000f0u;
-        fa[2] = va >> 8 & 0x000f000fu;
-        fa[3] = va >> 8 & 0x00f000f0u;
-        fb[0] = vb & 0x000f000fu;
-        fb[1] = vb & 0x00f000f0u;
-        fb[2] = vb >> 8 & 0x000f000fu;
-        fb[3] = vb >> 8 & 0x00f000f0u;
+        // symmetric codes are offset by 8
+        constexpr uint32_t lo = FMT == KQ_FMT_INT4_SYM ? 0x00080008u : 0u, hi = lo << 4;
+        fa[0] = (xa[j] & 0x000f000fu) ^ lo;
+        fa[1] = (xa[j] & 0x00f000f0u) ^ hi;
+        fa[2] = (xa[j] >> 8 & 0x000f000fu) ^ lo;
+        fa[3] = (xa[j] >> 8 & 0x00f000f0u) ^ hi;
+        fb[0] = (xb[j] & 0x000f000fu) ^ lo;
+        fb[1] = (xb[j] & 0x00f000f0u) ^ hi;
+        fb[2] = (xb[j] >> 8 & 0x000f000fu) ^ lo;
+        fb[3] = (xb[j] >> 8 & 0x00f000f0u) ^ hi;
       } else {
         e2m1_halves(xa[j], fa);
         e2m1_halves(xb[j], fb);
@@ -325,8 +367,7 @@ __device__ __forceinline__ void compute_unit(const Params& P, const Unit<FMT, kB
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        uint4 b = make_uint4(0, 0, 0, 0);
-        if (8 * n + g < cols) b = xs[((gl * NT + n) * 4 + j) * 32 + lane];
+        const uint4 b = xs[((gl * NT + n) * 4 + j) * 32 + lane];
         mma16816(c[n], fa[0], fb[0], fa[1], fb[1], b.x, b.y);
         mma16816(c[n], fa[2], fb[2], fa[3], fb[3], b.z, b.w);
       }
@@ -334,18 +375,17 @@ __device__ __forceinline__ void compute_unit(const Params& P, const Unit<FMT, kB
     // ---- the group's sums, scaled and added in fp32
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float2 f[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      if (8 * n + 2 * t < cols) f[0] = xf[gl * NT * 8 + 8 * n + 2 * t];
-      if (8 * n + 2 * t + 1 < cols) f[1] = xf[gl * NT * 8 + 8 * n + 2 * t + 1];
+      const float4 f4 = *reinterpret_cast<const float4*>(xf + gl * NT * 8 + 8 * n + 2 * t);
+      const float2 f[2] = {make_float2(f4.x, f4.y), make_float2(f4.z, f4.w)};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 q = f[e & 1];
         const uint32_t s = e < 2 ? u.sa[i] : u.sb[i];
         if (FMT == KQ_FMT_INT4_ASYM)
           acc[n][e] = fmaf(half_value(s & 0xffffu) * q.x,
-                           fmaf(-half_value(s >> 16), q.y, c[n][e] * 0x1p24f), acc[n][e]);
+                           fmaf(-half_value(s >> 16), q.y, c[n][e]), acc[n][e]);
         else if (FMT == KQ_FMT_INT4_SYM)
-          acc[n][e] = fmaf(q.x, fmaf(-8.0f, q.y, c[n][e] * 0x1p24f), acc[n][e]);
+          acc[n][e] = fmaf(q.x, fmaf(-8.0f, q.y, c[n][e]), acc[n][e]);
         else if (FMT == KQ_FMT_NVFP4)
           acc[n][e] = fmaf(q.x, c[n][e], acc[n][e]);
         else {
@@ -378,12 +418,11 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   // the others' shared memory may be written once they have all started
   if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   bool started = ranks == 1;
-  const int64_t row0 = (int64_t)(blockIdx.x / ranks) * P.tiles * 16;
-  const int tiles = (int)min((int64_t)P.tiles, (P.n - row0 + 15) / 16);
-  const int own = (P.tiles + ranks - 1) / ranks;          // tiles a CTA owns at most
+  const int64_t row0 = (int64_t)(blockIdx.x >> P.rank_shift) * P.tiles * 16;
+  const int tiles = (int)min((int64_t)P.tiles, (P.n - row0 + 15) >> 4);
+  const int own = (P.tiles + ranks - 1) >> P.rank_shift;  // tiles a CTA owns at most
   const int cols = P.x_bf16 ? P.m : 2 * P.m, mt = P.m;
-  const int gbegin = (int)((int64_t)rank * P.groups / ranks);
-  const int gend = (int)((int64_t)(rank + 1) * P.groups / ranks);
+  const int gbegin = rank_begin(P, rank), gend = rank_begin(P, rank + 1);
   for (int g0 = gbegin; g0 < gend; g0 += P.seg) {
     const int ng = min(P.seg, gend - g0), first_part = (g0 - gbegin) / kBatch;
     const int parts = (ng + kBatch - 1) / kBatch, units = tiles * parts;
@@ -394,7 +433,10 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
     };
     int i = warp;
     if (i < units) load(i);
-    if (g0 > gbegin) __syncthreads();     // the last segment's x is no longer read
+    if (g0 > gbegin)
+      __syncthreads();                    // the last segment's x is no longer read
+    else
+      clear_columns<NT>(P, cols, xs, xf);
     stage_x<INT4, NT>(P, g0, ng, xs, xf);
     __syncthreads();
     if (!started) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -404,9 +446,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
       const Unit<FMT, kBatch> now = u;
       if (i + kWarps < units) load(i + kWarps);
       float acc[NT][4];
-      compute_unit<FMT, NT, kBatch>(P, now, part * kBatch, ng, cols, xs, xf, acc);
-      const int owner = tile % ranks;
-      float* to = red + (size_t)(((rank * P.parts + first_part + part) * own + tile / ranks) * 16 +
+      compute_unit<FMT, NT, kBatch>(P, now, part * kBatch, ng, xs, xf, acc);
+      const int owner = tile & (ranks - 1);
+      float* to = red + (size_t)(((rank * P.parts + first_part + part) * own + (tile >> P.rank_shift)) * 16 +
                                  g) * mt;
       if (owner != rank) to = cg::this_cluster().map_shared_rank(to, owner);
 #pragma unroll
@@ -435,7 +477,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   }
   // ---- join: the ranks' batches in order; consecutive threads take consecutive
   // rows of one token
-  const int mine = (tiles - rank + ranks - 1) / ranks * 16;   // rows this CTA owns
+  const int mine = ((tiles - rank + ranks - 1) >> P.rank_shift) * 16;   // rows this CTA owns
   for (int i = threadIdx.x; i < mine * mt; i += Shape<NT>::kThreads) {
     const int tok = i / mine, r = i - tok * mine;
     const int64_t row = row0 + (int64_t)((r >> 4) * ranks + rank) * 16 + (r & 15);
@@ -443,12 +485,11 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
     const float* from = red + (size_t)r * mt + tok;
     float v = 0.0f;
     for (int c = 0; c < ranks; ++c) {
-      const int cg = (int)((int64_t)(c + 1) * P.groups / ranks) -
-                     (int)((int64_t)c * P.groups / ranks);
-      const int parts = (cg + kBatch - 1) / kBatch;
+      const int parts = (rank_begin(P, c + 1) - rank_begin(P, c) + kBatch - 1) / kBatch;
 #pragma unroll 4
       for (int w = 0; w < parts; ++w) v += from[(size_t)(c * P.parts + w) * own * 16 * mt];
     }
+    if (INT4) v *= 0x1p24f;               // the codes' 2^-24
     if (FMT == KQ_FMT_INT4_SYM) v *= static_cast<const float*>(P.scales)[row];
     if (FMT == KQ_FMT_NVFP4) v *= *P.tscale;
     const int64_t at = (int64_t)tok * P.n + row;
@@ -473,6 +514,7 @@ cudaError_t launch(Params P, cudaStream_t s) {
   while (ranks < KQ_RANKS && P.groups / (2 * ranks) >= kBatch) ranks *= 2;
   while (ranks < 8 && P.groups / ranks > 128) ranks *= 2;
   P.ranks = ranks;
+  for (P.rank_shift = 0; 1 << P.rank_shift < ranks;) ++P.rank_shift;
   const int64_t all = (P.n + 15) / 16, ctas = Shape<NT>::kCtas * sms;
   // x of a CTA's groups in one piece where 64 KB (128 KB for one CTA an SM) hold it
   const int mine = (P.groups + ranks - 1) / ranks;
@@ -480,6 +522,11 @@ cudaError_t launch(Params P, cudaStream_t s) {
   P.seg = P.parts * kBatch;
   const int most = 131072 / Shape<NT>::kCtas / (2048 * NT);
   if (P.seg > most) P.seg = most;
+  // the scales of kBatch groups are one aligned load where every range and row
+  // begins at a multiple of kBatch groups
+  P.wide = P.groups % (kBatch * ranks) == 0 &&
+           (reinterpret_cast<uintptr_t>(P.scales) | reinterpret_cast<uintptr_t>(P.zeros)) %
+                   (2 * kBatch) == 0;
   // rows for one round of CTAs, as far as their sums fit 32 KB
   int64_t tiles = (all * ranks + ctas - 1) / ctas;
   const int64_t cap = 32768 / ((int64_t)P.parts * P.m * 64);
@@ -519,7 +566,7 @@ cudaError_t launch_gemv(int fmt, const void* x, int x_bf16, int m, const uint8_t
                         const void* scales, const void* zeros, const float* tscale, int64_t n,
                         int k, void* y, int y_bf16, cudaStream_t s) {
   const gv::Params P{x, codes, scales, static_cast<const uint16_t*>(zeros), tscale, y, n, m, k,
-                     (k + 127) / 128, x_bf16, y_bf16, 0, 0, 0, 1};
+                     (k + 127) / 128, x_bf16, y_bf16, 0, 0, 0, 1, 0, 0};
   switch (fmt) {
     case KQ_FMT_INT4_SYM: return gv::launch_tiles<KQ_FMT_INT4_SYM>(P, s);
     case KQ_FMT_INT4_ASYM: return gv::launch_tiles<KQ_FMT_INT4_ASYM>(P, s);
