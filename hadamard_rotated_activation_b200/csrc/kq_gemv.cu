@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "kq.h"
@@ -127,22 +128,13 @@ __device__ __forceinline__ Eight load8(const Params& P, int tok, int k0) {
   return e;
 }
 
-// Zeros in the columns behind the last one (once; nothing else writes them).
-template <int NT>
-__device__ __forceinline__ void clear_columns(const Params& P, int cols, uint4* xs, float2* xf) {
-  constexpr int kThreads = Shape<NT>::kThreads;
-  if (cols == 8 * NT) return;
-  for (int i = threadIdx.x; i < P.seg * NT * 128; i += kThreads)
-    if ((i >> 2 & 7) + 8 * (i >> 7 & (NT - 1)) >= cols) xs[i] = make_uint4(0, 0, 0, 0);
-  for (int i = threadIdx.x; i < P.seg * NT * 8; i += kThreads)
-    if ((i & (8 * NT - 1)) >= cols) xf[i] = make_float2(0.0f, 0.0f);
-}
-
 // Stages x of groups [g0, g0 + ng) for the columns of NT mma tiles.  16 lanes take
 // one (group, token), a lane 8 consecutive elements, which are one 16-byte piece
 // in fragment order: (group, tile, word j, column, t) holds elements 32 t + 8 j ...
 // as pairs (0,4) (1,5) (2,6) (3,7) for the masked INT4 codes, whose odd ones
-// carry a factor 16, or in their own order for the converted E2M1 codes.
+// carry a factor 16, or in their own order for the converted E2M1 codes.  Columns
+// behind the last one are left as they are: what they hold reaches no other
+// column, and their sums are not stored.
 template <bool INT4, int NT>
 __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, uint4* xs, float2* xf) {
   constexpr int kAhead = 4;
@@ -421,7 +413,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   const int64_t row0 = (int64_t)(blockIdx.x >> P.rank_shift) * P.tiles * 16;
   const int tiles = (int)min((int64_t)P.tiles, (P.n - row0 + 15) >> 4);
   const int own = (P.tiles + ranks - 1) >> P.rank_shift;  // tiles a CTA owns at most
-  const int cols = P.x_bf16 ? P.m : 2 * P.m, mt = P.m;
+  const int mt = P.m;
   const int gbegin = rank_begin(P, rank), gend = rank_begin(P, rank + 1);
   for (int g0 = gbegin; g0 < gend; g0 += P.seg) {
     const int ng = min(P.seg, gend - g0), first_part = (g0 - gbegin) / kBatch;
@@ -433,10 +425,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
     };
     int i = warp;
     if (i < units) load(i);
-    if (g0 > gbegin)
-      __syncthreads();                    // the last segment's x is no longer read
-    else
-      clear_columns<NT>(P, cols, xs, xf);
+    if (g0 > gbegin) __syncthreads();     // the last segment's x is no longer read
     stage_x<INT4, NT>(P, g0, ng, xs, xf);
     __syncthreads();
     if (!started) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -503,19 +492,55 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
 #ifndef KQ_RANKS
 #define KQ_RANKS 4
 #endif
+constexpr size_t kMostX = 65536 + 2048, kMostSums = 32768;   // shared memory of a CTA
+
+// CTAs of clusters of `ranks` that the current device holds at a time: a cluster
+// stays within a GPC, so it is less than all SMs hold.  Looked up once.
+template <int FMT, int NT>
+cudaError_t resident_ctas(int ranks, int* out) {
+  // the attribute set here holds for every launch of this kernel on the device
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][4];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int i = ranks == 1 ? 0 : ranks == 2 ? 1 : ranks == 4 ? 2 : 3;
+  if (dev < kDevices && (*out = known[dev][i].load(std::memory_order_relaxed)) > 0)
+    return cudaSuccess;
+  const size_t smem = Shape<NT>::kCtas == 1 ? 2 * kMostX + kMostSums : kMostX + kMostSums;
+  e = cudaFuncSetAttribute((const void*)k_gemv<FMT, NT>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ranks);
+  cfg.blockDim = dim3(Shape<NT>::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  e = cudaOccupancyMaxActiveClusters(&clusters, (const void*)k_gemv<FMT, NT>, &cfg);
+  if (e != cudaSuccess) return e;
+  *out = clusters * ranks;
+  if (dev < kDevices) known[dev][i].store(*out, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 template <int FMT, int NT>
 cudaError_t launch(Params P, cudaStream_t s) {
   constexpr int kBatch = Shape<NT>::kBatch;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   int ranks = 1;
   while (ranks < KQ_RANKS && P.groups / (2 * ranks) >= kBatch) ranks *= 2;
   while (ranks < 8 && P.groups / ranks > 128) ranks *= 2;
   P.ranks = ranks;
   for (P.rank_shift = 0; 1 << P.rank_shift < ranks;) ++P.rank_shift;
-  const int64_t all = (P.n + 15) / 16, ctas = Shape<NT>::kCtas * sms;
+  int ctas = 0;
+  cudaError_t e = resident_ctas<FMT, NT>(ranks, &ctas);
+  if (e != cudaSuccess) return e;
+  const int64_t all = (P.n + 15) / 16;
   // x of a CTA's groups in one piece where 64 KB (128 KB for one CTA an SM) hold it
   const int mine = (P.groups + ranks - 1) / ranks;
   P.parts = (mine + kBatch - 1) / kBatch;
@@ -528,16 +553,13 @@ cudaError_t launch(Params P, cudaStream_t s) {
            (reinterpret_cast<uintptr_t>(P.scales) | reinterpret_cast<uintptr_t>(P.zeros)) %
                    (2 * kBatch) == 0;
   // rows for one round of CTAs, as far as their sums fit 32 KB
-  int64_t tiles = (all * ranks + ctas - 1) / ctas;
-  const int64_t cap = 32768 / ((int64_t)P.parts * P.m * 64);
+  int64_t tiles = (all + ctas / ranks - 1) / (ctas / ranks);
+  const int64_t cap = kMostSums / ((int64_t)P.parts * P.m * 64);
   if (tiles > cap) tiles = cap;
   P.tiles = (int)(tiles < 1 ? 1 : tiles);
   const int own = (P.tiles + ranks - 1) / ranks;
   const size_t smem = (size_t)P.seg * NT * (2048 + 64) +
                       sizeof(float) * ranks * P.parts * own * 16 * P.m;
-  e = cudaFuncSetAttribute((const void*)k_gemv<FMT, NT>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((all + P.tiles - 1) / P.tiles * ranks));
   cfg.blockDim = dim3(Shape<NT>::kThreads);
