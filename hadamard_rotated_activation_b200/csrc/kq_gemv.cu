@@ -42,15 +42,19 @@ namespace gv {
 namespace cg = cooperative_groups;
 using sm100::pow2f;
 
-// Up to two tiles of 8 columns: two CTAs of 8 warps an SM and units of 4 groups.
-// Four tiles: one CTA of 16 warps, which stages x once an SM, and units of 2
-// groups, so that two of them fit the registers beside the sums.
+// A warp streams its rows in steps of 16 rows by kStep groups, kStages of which are
+// on their way or in use.  Up to two tiles of 8 columns: two CTAs of 8 warps an
+// SM.  Four tiles: one CTA of 16 warps, which stages x once an SM.
+constexpr int kStep = 2;
+constexpr int kRow = kStep * 64;                  // bytes of a staged row of codes
+constexpr int kScaleRow = kStep * 8;              // bytes of its scales at most
+constexpr int kStage = 16 * (kRow + kScaleRow);
 template <int NT>
 struct Shape {
   static constexpr int kWarps = NT == 4 ? 16 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = NT == 4 ? 1 : 2;
-  static constexpr int kBatch = NT == 4 ? 2 : 4;
+  static constexpr int kStages = NT == 4 ? 3 : 4;
 };
 
 struct Params {
@@ -65,9 +69,10 @@ struct Params {
   int x_bf16, y_bf16;
   int tiles;                              // 16-row tiles of a cluster
   int seg;                                // groups whose x is staged at a time
-  int parts;                              // batches of a CTA: sums kept apart
+  int parts;                              // warps that share a tile's groups in a CTA
   int ranks, rank_shift;                  // CTAs of a cluster, which split k: 2^rank_shift
-  int wide;                               // scales of kBatch groups in one load
+  int wide;                               // scales of a step's row by aligned copies
+  uint32_t recip;                         // 2^16 / m, rounded up
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -96,12 +101,14 @@ __device__ __forceinline__ float half_value(uint32_t h) {
   return __half2float(__ushort_as_half((unsigned short)h));
 }
 
-// Codes are read once: not kept in L1, whole lines fetched into L2.
-__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool in = true) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;"
+                 :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                 :: "r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   uint32_t d;
@@ -137,7 +144,7 @@ __device__ __forceinline__ Eight load8(const Params& P, int tok, int k0) {
 // column, and their sums are not stored.
 template <bool INT4, int NT>
 __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, uint4* xs, float2* xf) {
-  constexpr int kAhead = 4;
+  constexpr int kAhead = NT == 1 ? 2 : 4;
   const int lane16 = threadIdx.x & 15, slot = threadIdx.x >> 4;
   const int items = ng * P.m;
   constexpr int kThreads = Shape<NT>::kThreads;
@@ -145,12 +152,14 @@ __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, uint4* 
     Eight in[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int i = i0 + u * (kThreads / 16), gi = i / P.m, tok = i - gi * P.m;
+      const int i = i0 + u * (kThreads / 16);
+      const int gi = (int)(i * P.recip >> 16), tok = i - gi * P.m;
       in[u] = load8(P, i < items ? tok : P.m, (g0 + gi) * 128 + 8 * lane16);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int i = i0 + u * (kThreads / 16), gi = i / P.m, tok = i - gi * P.m;
+      const int i = i0 + u * (kThreads / 16);
+      const int gi = (int)(i * P.recip >> 16), tok = i - gi * P.m;
       if (__all_sync(0xffffffffu, i >= items)) break;
       float v[8];
       if (P.x_bf16) {
@@ -219,120 +228,133 @@ __device__ __forceinline__ int rank_begin(const Params& P, int rank) {
   return (int)((uint32_t)(rank * P.groups) >> P.rank_shift);
 }
 
-// A unit of work as loaded: 16 rows (g and g + 8 of a lane) by kBatch groups.
-template <int FMT, int kBatch>
-struct Unit {
-  uint4 a[kBatch], b[kBatch];
-  uint32_t sa[kBatch], sb[kBatch];        // fp16 scale | zero << 16; E4M3 pair; E8M0 byte
-};
-template <int FMT, int kBatch>
-__device__ __forceinline__ void load_unit(const Params& P, int64_t row0, int g0, int gend,
-                                          Unit<FMT, kBatch>& u) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t last = P.n - 1;
-  const int64_t ra = min(row0 + g, last), rb = min(row0 + 8 + g, last);
-  const uint8_t* ca = P.codes + ra * (P.k / 2) + 16 * t + (int64_t)g0 * 64;
-  const uint8_t* cb = P.codes + rb * (P.k / 2) + 16 * t + (int64_t)g0 * 64;
-#pragma unroll
-  for (int i = 0; i < kBatch; ++i) {
-    const int gi = g0 + i;
-    u.a[i] = u.b[i] = make_uint4(0, 0, 0, 0);
-    if (gi < gend && gi * 128 + 32 * t < P.k) {
-      u.a[i] = load_codes(ca + i * 64);
-      u.b[i] = load_codes(cb + i * 64);
-    }
-  }
-  if (P.wide && FMT == KQ_FMT_INT4_ASYM) {
-    const uint16_t* s16 = static_cast<const uint16_t*>(P.scales) + g0;
-    const uint16_t* z16 = P.zeros + g0;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int64_t at = (r ? rb : ra) * P.groups;
-      uint32_t* to = r ? u.sb : u.sa;
-      uint32_t sw[kBatch / 2], zw[kBatch / 2];
-      if constexpr (kBatch == 4) {
-        const uint2 a = __ldg(reinterpret_cast<const uint2*>(s16 + at));
-        const uint2 b = __ldg(reinterpret_cast<const uint2*>(z16 + at));
-        sw[0] = a.x;
-        sw[1] = a.y;
-        zw[0] = b.x;
-        zw[1] = b.y;
-      } else {
-        sw[0] = __ldg(reinterpret_cast<const uint32_t*>(s16 + at));
-        zw[0] = __ldg(reinterpret_cast<const uint32_t*>(z16 + at));
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        to[i] = __byte_perm(sw[i / 2], zw[i / 2], i & 1 ? 0x7632 : 0x5410);
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < kBatch; ++i) {
-    const int gi = g0 + i;
-    u.sa[i] = u.sb[i] = 0;
-    if (gi < gend && gi * 128 + 32 * t < P.k) {
-      if (FMT == KQ_FMT_INT4_ASYM) {
-        const uint16_t* s16 = static_cast<const uint16_t*>(P.scales) + gi;
-        const uint16_t* z16 = P.zeros + gi;
-        u.sa[i] = __ldg(s16 + ra * P.groups) | (uint32_t)__ldg(z16 + ra * P.groups) << 16;
-        u.sb[i] = __ldg(s16 + rb * P.groups) | (uint32_t)__ldg(z16 + rb * P.groups) << 16;
-      } else if (FMT == KQ_FMT_NVFP4) {
-        const uint16_t* s16 = static_cast<const uint16_t*>(P.scales) + gi * 4 + t;
-        u.sa[i] = __ldg(s16 + ra * (P.k / 32));
-        u.sb[i] = __ldg(s16 + rb * (P.k / 32));
-      } else if (FMT == KQ_FMT_MXFP4) {
-        const uint8_t* s8 = static_cast<const uint8_t*>(P.scales) + gi * 4 + t;
-        u.sa[i] = __ldg(s8 + ra * (P.k / 32));
-        u.sb[i] = __ldg(s8 + rb * (P.k / 32));
-      }
-    }
-  }
-}
+// A warp's stream through the codes: the rows it is at, and the lane's share of
+// the copies of a step.  8 lanes a row, 4 rows at a time; the 16-byte piece c of row
+// r is staged at c ^ 4 (r & 1), which keeps the fragment reads (two rows by four
+// pieces at a time) free of bank conflicts.
+template <int FMT>
+struct Stream {
+  const uint8_t* codes;                   // row0, the lane's piece
+  const uint8_t* scales;                  // the lane's row of scales (zero points)
+  int off[4];                             // bytes to the lane's rows (the last row again behind it)
+  int64_t row0;
 
-template <int FMT, int NT, int kBatch>
-__device__ __forceinline__ void compute_unit(const Params& P, const Unit<FMT, kBatch>& u, int gl0, int ng,
-                                             const uint4* xs, const float2* xf,
-                                             float (&acc)[NT][4]) {
+  __device__ __forceinline__ void start(const Params& P, int64_t row) {
+    const int lane = threadIdx.x & 31;
+    const int left = (int)min(P.n - 1 - row, (int64_t)15);
+    row0 = row;
+    codes = P.codes + row * (P.k / 2) + 16 * (lane & 7);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) off[i] = min(left, 4 * i + (lane >> 3)) * (P.k / 2);
+    const int64_t sr = row + min(left, lane & 15);
+    if (FMT == KQ_FMT_INT4_ASYM)
+      scales = reinterpret_cast<const uint8_t*>(
+          (lane < 16 ? static_cast<const uint16_t*>(P.scales) : P.zeros) + sr * P.groups);
+    else if (FMT == KQ_FMT_NVFP4)
+      scales = static_cast<const uint8_t*>(P.scales) + sr * (P.k / 16);
+    else if (FMT == KQ_FMT_MXFP4)
+      scales = static_cast<const uint8_t*>(P.scales) + sr * (P.k / 32);
+  }
+
+  // Starts the copies of groups g0 ... (none at or behind gend) into a stage: codes,
+  // behind them 16 rows of scales: INT4 asymmetric kStep fp16 scales and zero
+  // points, NVFP4 8 E4M3 bytes a group, MXFP4 4 E8M0 bytes a group.
+  __device__ __forceinline__ void copy(const Params& P, int g0, int gend, uint8_t* stage) const {
+    const int lane = threadIdx.x & 31, c = lane & 7, r = lane >> 3;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(stage);
+    const bool in = g0 + (c >> 2) < gend && g0 * 128 + 32 * c < P.k;
+    const uint8_t* from = codes + (in ? g0 * 64 : 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      copy_async<16>(to + (4 * i + r) * kRow + 16 * (c ^ ((r & 1) << 2)), from + off[i], in);
+    if (FMT == KQ_FMT_INT4_SYM) return;
+    const uint32_t ts = to + 16 * kRow + (lane & 15) * kScaleRow;
+    if (P.wide) {
+      if (FMT == KQ_FMT_INT4_ASYM)
+        copy_async<4>(ts + (lane >> 4) * 4, scales + 2 * g0);
+      else if (lane < 16)
+        copy_async<FMT == KQ_FMT_NVFP4 ? 16 : 8>(ts, scales + (FMT == KQ_FMT_NVFP4 ? 8 : 4) * g0);
+      return;
+    }
+    // scales that no aligned copy reaches: one by one
+    const int per = FMT == KQ_FMT_INT4_ASYM ? 1 : FMT == KQ_FMT_NVFP4 ? 8 : 4;   // a group
+    const int count = FMT == KQ_FMT_INT4_ASYM ? P.groups : FMT == KQ_FMT_NVFP4 ? P.k / 16 : P.k / 32;
+    const int left = (int)min(P.n - 1 - row0, (int64_t)15);
+    for (int i = lane; i < 16 * kStep * per; i += 32) {
+      const int row = i / (kStep * per), e = i - row * (kStep * per), at = g0 * per + e;
+      const int64_t src = (row0 + min(left, row)) * count + at;
+      const bool ok = at < gend * per && at < count;
+      uint8_t* d = stage + 16 * kRow + row * kScaleRow;
+      if (FMT == KQ_FMT_INT4_ASYM) {
+        reinterpret_cast<uint16_t*>(d)[e] =
+            ok ? __ldg(static_cast<const uint16_t*>(P.scales) + src) : 0;
+        reinterpret_cast<uint16_t*>(d)[kStep + e] = ok ? __ldg(P.zeros + src) : 0;
+      } else {
+        d[e] = ok ? __ldg(static_cast<const uint8_t*>(P.scales) + src) : 0;
+      }
+    }
+  }
+};
+
+// Adds a staged step: its first ng groups, times groups gl ... of the staged x.
+template <int FMT, int NT>
+__device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int ng, const uint4* xs,
+                                             const float2* xf, float (&acc)[NT][4]) {
   constexpr bool INT4 = FMT == KQ_FMT_INT4_SYM || FMT == KQ_FMT_INT4_ASYM;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint8_t* ca = stage + g * kRow + 16 * t;
+  const uint8_t* sca = stage + 16 * kRow + g * kScaleRow;
+  constexpr int kDown = 8 * kScaleRow;            // from row g to row g + 8
+  const uint4* xg = xs + gl * NT * 128 + lane;
+  const float2* fg = xf + gl * NT * 8 + 2 * t;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kBatch; ++i) {
-    const int gl = gl0 + i;               // group within the staged segment
-    if (gl >= ng) break;
+  for (int i = 0; i < kStep; ++i, xg += NT * 128, fg += NT * 8) {
+    if (i >= ng) break;
+    const int at = 64 * (i ^ (g & 1));
+    const uint4 wa = *reinterpret_cast<const uint4*>(ca + at);
+    const uint4 wb = *reinterpret_cast<const uint4*>(ca + 8 * kRow + at);
+    const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
     float c[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) c[n][j] = 0.0f;
-    const uint32_t xa[4] = {u.a[i].x, u.a[i].y, u.a[i].z, u.a[i].w};
-    const uint32_t xb[4] = {u.b[i].x, u.b[i].y, u.b[i].z, u.b[i].w};
-    uint32_t ea = 0, eb = 0;              // MXFP4: largest exponent byte of the row's blocks
     uint32_t ma[2] = {0, 0}, mb[2] = {0, 0};
-    if (FMT == KQ_FMT_NVFP4) {
+    float sa = 1.0f, sb = 1.0f, za = 0.0f, zb = 0.0f;
+    if (FMT == KQ_FMT_INT4_ASYM) {
+      const uint16_t* s16 = reinterpret_cast<const uint16_t*>(sca) + i;
+      sa = half_value(s16[0]);
+      za = half_value(s16[kStep]);
+      sb = half_value(s16[kDown / 2]);
+      zb = half_value(s16[kDown / 2 + kStep]);
+    } else if (FMT == KQ_FMT_INT4_SYM) {
+      za = zb = 8.0f;
+    } else if (FMT == KQ_FMT_NVFP4) {
       // both blocks' E4M3 scales as fp16, each in both halves
+      const uint32_t ba = *reinterpret_cast<const uint16_t*>(sca + 8 * i + 2 * t);
+      const uint32_t bb = *reinterpret_cast<const uint16_t*>(sca + kDown + 8 * i + 2 * t);
       uint32_t ha, hb;
-      asm("{.reg .b16 v; cvt.u16.u32 v, %1; cvt.rn.f16x2.e4m3x2 %0, v;}" : "=r"(ha) : "r"(u.sa[i]));
-      asm("{.reg .b16 v; cvt.u16.u32 v, %1; cvt.rn.f16x2.e4m3x2 %0, v;}" : "=r"(hb) : "r"(u.sb[i]));
+      asm("{.reg .b16 v; cvt.u16.u32 v, %1; cvt.rn.f16x2.e4m3x2 %0, v;}" : "=r"(ha) : "r"(ba));
+      asm("{.reg .b16 v; cvt.u16.u32 v, %1; cvt.rn.f16x2.e4m3x2 %0, v;}" : "=r"(hb) : "r"(bb));
       ma[0] = __byte_perm(ha, 0, 0x1010);
       ma[1] = __byte_perm(ha, 0, 0x3232);
       mb[0] = __byte_perm(hb, 0, 0x1010);
       mb[1] = __byte_perm(hb, 0, 0x3232);
-    } else if (FMT == KQ_FMT_MXFP4) {
-      ea = max(u.sa[i], __shfl_xor_sync(0xffffffffu, u.sa[i], 1));
+    } else {
+      // relative to the largest of the row's four blocks
+      const uint32_t ba = sca[4 * i + t], bb = sca[kDown + 4 * i + t];
+      uint32_t ea = max(ba, __shfl_xor_sync(0xffffffffu, ba, 1));
+      uint32_t eb = max(bb, __shfl_xor_sync(0xffffffffu, bb, 1));
       ea = max(ea, __shfl_xor_sync(0xffffffffu, ea, 2));
-      eb = max(u.sb[i], __shfl_xor_sync(0xffffffffu, u.sb[i], 1));
       eb = max(eb, __shfl_xor_sync(0xffffffffu, eb, 2));
-      auto down = [](uint32_t d) {        // 2^-d in both halves
-        const uint32_t h = d < 15 ? (15 - d) << 10 : d < 25 ? 1u << (24 - d) : 0u;
-        return h | h << 16;
+      auto down = [](uint32_t d) {        // 2^-d in both halves, 0 for d > 24
+        const float f = __uint_as_float((127u - min(d, 100u)) << 23);
+        return half2_bits(f, f);
       };
-      ma[0] = ma[1] = down(ea - u.sa[i]);
-      mb[0] = mb[1] = down(eb - u.sb[i]);
+      ma[0] = ma[1] = down(ea - ba);
+      mb[0] = mb[1] = down(eb - bb);
+      sa = __uint_as_float(ea ? ea << 23 : 0x00400000u);
+      sb = __uint_as_float(eb ? eb << 23 : 0x00400000u);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -359,7 +381,7 @@ __device__ __forceinline__ void compute_unit(const Params& P, const Unit<FMT, kB
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint4 b = xs[((gl * NT + n) * 4 + j) * 32 + lane];
+        const uint4 b = xg[(n * 4 + j) * 32];
         mma16816(c[n], fa[0], fb[0], fa[1], fb[1], b.x, b.y);
         mma16816(c[n], fa[2], fb[2], fa[3], fb[3], b.z, b.w);
       }
@@ -367,45 +389,46 @@ __device__ __forceinline__ void compute_unit(const Params& P, const Unit<FMT, kB
     // ---- the group's sums, scaled and added in fp32
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float4 f4 = *reinterpret_cast<const float4*>(xf + gl * NT * 8 + 8 * n + 2 * t);
-      const float2 f[2] = {make_float2(f4.x, f4.y), make_float2(f4.z, f4.w)};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 q = f[e & 1];
-        const uint32_t s = e < 2 ? u.sa[i] : u.sb[i];
-        if (FMT == KQ_FMT_INT4_ASYM)
-          acc[n][e] = fmaf(half_value(s & 0xffffu) * q.x,
-                           fmaf(-half_value(s >> 16), q.y, c[n][e]), acc[n][e]);
-        else if (FMT == KQ_FMT_INT4_SYM)
-          acc[n][e] = fmaf(q.x, fmaf(-8.0f, q.y, c[n][e]), acc[n][e]);
-        else if (FMT == KQ_FMT_NVFP4)
-          acc[n][e] = fmaf(q.x, c[n][e], acc[n][e]);
-        else {
-          const uint32_t eb8 = e < 2 ? ea : eb;
-          const float p = __uint_as_float(eb8 ? eb8 << 23 : 0x00400000u);
-          acc[n][e] = fmaf(c[n][e] * q.x, p, acc[n][e]);
-        }
+      const float4 f = *reinterpret_cast<const float4*>(fg + 8 * n);
+      if (INT4) {
+        acc[n][0] = fmaf(sa * f.x, fmaf(-za, f.y, c[n][0]), acc[n][0]);
+        acc[n][1] = fmaf(sa * f.z, fmaf(-za, f.w, c[n][1]), acc[n][1]);
+        acc[n][2] = fmaf(sb * f.x, fmaf(-zb, f.y, c[n][2]), acc[n][2]);
+        acc[n][3] = fmaf(sb * f.z, fmaf(-zb, f.w, c[n][3]), acc[n][3]);
+      } else if (FMT == KQ_FMT_NVFP4) {
+        acc[n][0] = fmaf(f.x, c[n][0], acc[n][0]);
+        acc[n][1] = fmaf(f.z, c[n][1], acc[n][1]);
+        acc[n][2] = fmaf(f.x, c[n][2], acc[n][2]);
+        acc[n][3] = fmaf(f.z, c[n][3], acc[n][3]);
+      } else {
+        acc[n][0] = fmaf(c[n][0] * f.x, sa, acc[n][0]);
+        acc[n][1] = fmaf(c[n][1] * f.z, sa, acc[n][1]);
+        acc[n][2] = fmaf(c[n][2] * f.x, sb, acc[n][2]);
+        acc[n][3] = fmaf(c[n][3] * f.z, sb, acc[n][3]);
       }
     }
   }
 }
 
-// A cluster takes 16 P.tiles rows and all of k, a CTA of it a range of k.  x of
-// that range is staged once (in segments where k is long), while the first
-// units' codes are on their way; then the warps take units, the next one's codes
-// loaded before this one is computed.  Every unit's sums go to a place of their
+// A cluster takes 16 P.tiles rows and all of k, a CTA of it a range of k, a warp
+// (tile, part) units: a tile by its part of the range.  Each warp keeps kStages
+// steps of its units on their way by asynchronous copies into shared memory, with
+// no barrier between warps; x of the range is staged once (in segments where k is
+// long) while the first ones come in.  Every unit's sums go to a place of their
 // own in the shared memory of the CTA that owns the tile; behind one cluster
 // barrier the owners add them up in order.  (Measured instead: sums read from the
 // others' shared memory behind the barrier cost 0.5 us a CTA of the cluster.)
 template <int FMT, int NT>
 __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(Params P) {
+  using S = Shape<NT>;
   constexpr bool INT4 = FMT == KQ_FMT_INT4_SYM || FMT == KQ_FMT_INT4_ASYM;
-  constexpr int kBatch = Shape<NT>::kBatch, kWarps = Shape<NT>::kWarps;
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kWarps = S::kWarps;
+  extern __shared__ __align__(128) uint8_t smem[];
   const int ranks = P.ranks, rank = ranks > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint4* xs = reinterpret_cast<uint4*>(smem);
-  float2* xf = reinterpret_cast<float2*>(smem + (size_t)P.seg * NT * 2048);
+  uint8_t* ring = smem + warp * (S::kStages * kStage);
+  uint4* xs = reinterpret_cast<uint4*>(smem + kWarps * S::kStages * kStage);
+  float2* xf = reinterpret_cast<float2*>(xs + P.seg * NT * 128);
   float* red = reinterpret_cast<float*>(xf + P.seg * NT * 8);
   // the others' shared memory may be written once they have all started
   if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -413,51 +436,87 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   const int64_t row0 = (int64_t)(blockIdx.x >> P.rank_shift) * P.tiles * 16;
   const int tiles = (int)min((int64_t)P.tiles, (P.n - row0 + 15) >> 4);
   const int own = (P.tiles + ranks - 1) >> P.rank_shift;  // tiles a CTA owns at most
-  const int mt = P.m;
+  const int mt = P.m, parts = P.parts;
   const int gbegin = rank_begin(P, rank), gend = rank_begin(P, rank + 1);
   for (int g0 = gbegin; g0 < gend; g0 += P.seg) {
-    const int ng = min(P.seg, gend - g0), first_part = (g0 - gbegin) / kBatch;
-    const int parts = (ng + kBatch - 1) / kBatch, units = tiles * parts;
-    Unit<FMT, kBatch> u;
-    auto load = [&](int i) {
-      const int tile = i / parts, part = i - tile * parts;
-      load_unit<FMT, kBatch>(P, row0 + 16 * tile, g0 + part * kBatch, g0 + ng, u);
+    const int ng = min(P.seg, gend - g0), steps = (ng + kStep - 1) / kStep;
+    const int units = tiles * parts;
+    // the steps of a part: an even share of the segment's
+    auto from = [&](int part) { return (int)((uint32_t)(part * steps) / (uint32_t)parts); };
+    int funit = warp, fstep = 0, fend = 0, fill = 0;      // copied next
+    Stream<FMT> stream;
+    auto open = [&] {
+      while (funit < units) {
+        const int tile = funit / parts, part = funit - tile * parts;
+        fstep = from(part);
+        fend = from(part + 1);
+        stream.start(P, row0 + 16 * tile);
+        if (fstep < fend) return;
+        funit += kWarps;
+      }
     };
-    int i = warp;
-    if (i < units) load(i);
+    auto fetch = [&] {
+      if (funit < units) {
+        stream.copy(P, g0 + fstep * kStep, g0 + ng, ring + fill * kStage);
+        if (++fill == S::kStages) fill = 0;
+        if (++fstep == fend) {
+          funit += kWarps;
+          open();
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    open();
+#pragma unroll 1
+    for (int i = 0; i < S::kStages; ++i) fetch();
     if (g0 > gbegin) __syncthreads();     // the last segment's x is no longer read
     stage_x<INT4, NT>(P, g0, ng, xs, xf);
     __syncthreads();
     if (!started) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     started = true;
-    for (; i < units; i += kWarps) {
-      const int tile = i / parts, part = i - tile * parts;
-      const Unit<FMT, kBatch> now = u;
-      if (i + kWarps < units) load(i + kWarps);
+    int stage = 0;
+#pragma unroll 1
+    for (int unit = warp; unit < units; unit += kWarps) {
+      const int tile = unit / parts, part = unit - tile * parts;
+      const int s1 = from(part + 1);
       float acc[NT][4];
-      compute_unit<FMT, NT, kBatch>(P, now, part * kBatch, ng, xs, xf, acc);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
+#pragma unroll 1
+      for (int step = from(part); step < s1; ++step) {
+        asm volatile("cp.async.wait_group %0;" :: "n"(S::kStages - 1) : "memory");
+        __syncwarp();
+        compute_step<FMT, NT>(ring + stage * kStage, step * kStep, ng - step * kStep, xs, xf, acc);
+        __syncwarp();                     // the stage is free
+        if (++stage == S::kStages) stage = 0;
+        fetch();
+      }
       const int owner = tile & (ranks - 1);
-      float* to = red + (size_t)(((rank * P.parts + first_part + part) * own + (tile >> P.rank_shift)) * 16 +
-                                 g) * mt;
+      float* to = red + (((rank * parts + part) * own + (tile >> P.rank_shift)) * 16 + g) * mt;
       if (owner != rank) to = cg::this_cluster().map_shared_rank(to, owner);
+      // behind the first segment: on top of what the same lane put there
+      auto put = [&](float* at, float v) { *at = g0 > gbegin ? *at + v : v; };
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         if (P.x_bf16) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int tok = 8 * n + 2 * t + (e & 1);
-            if (tok < mt) to[8 * (e >> 1) * mt + tok] = acc[n][e];
+            if (tok < mt) put(to + 8 * (e >> 1) * mt + tok, acc[n][e]);
           }
         } else {
           const int tok = 4 * n + t;
           if (tok < mt) {
-            to[tok] = acc[n][0] + acc[n][1];
-            to[8 * mt + tok] = acc[n][2] + acc[n][3];
+            put(to + tok, acc[n][0] + acc[n][1]);
+            put(to + 8 * mt + tok, acc[n][2] + acc[n][3]);
           }
         }
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if (ranks > 1) {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -473,11 +532,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
     if (row >= P.n) continue;
     const float* from = red + (size_t)r * mt + tok;
     float v = 0.0f;
-    for (int c = 0; c < ranks; ++c) {
-      const int parts = (rank_begin(P, c + 1) - rank_begin(P, c) + kBatch - 1) / kBatch;
 #pragma unroll 4
-      for (int w = 0; w < parts; ++w) v += from[(size_t)(c * P.parts + w) * own * 16 * mt];
-    }
+    for (int c = 0; c < ranks * parts; ++c) v += from[(size_t)c * own * 16 * mt];
     if (INT4) v *= 0x1p24f;               // the codes' 2^-24
     if (FMT == KQ_FMT_INT4_SYM) v *= static_cast<const float*>(P.scales)[row];
     if (FMT == KQ_FMT_NVFP4) v *= *P.tscale;
@@ -492,7 +548,15 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
 #ifndef KQ_RANKS
 #define KQ_RANKS 4
 #endif
-constexpr size_t kMostX = 65536 + 2048, kMostSums = 32768;   // shared memory of a CTA
+// Shared memory of a CTA: the stages, x of a segment, the sums.
+template <int NT>
+struct Room {
+  static constexpr int kAll = (Shape<NT>::kCtas == 1 ? 227 : 113) * 1024;
+  static constexpr int kRings = Shape<NT>::kWarps * Shape<NT>::kStages * kStage;
+  static constexpr int kSums = 12 * 1024;
+  static constexpr int kGroups = (kAll - kRings - kSums) / (NT * (2048 + 64)) / kStep * kStep;
+  static_assert(kGroups >= 4, "room for x");
+};
 
 // CTAs of clusters of `ranks` that the current device holds at a time: a cluster
 // stays within a GPC, so it is less than all SMs hold.  Looked up once.
@@ -507,7 +571,7 @@ cudaError_t resident_ctas(int ranks, int* out) {
   const int i = ranks == 1 ? 0 : ranks == 2 ? 1 : ranks == 4 ? 2 : 3;
   if (dev < kDevices && (*out = known[dev][i].load(std::memory_order_relaxed)) > 0)
     return cudaSuccess;
-  const size_t smem = Shape<NT>::kCtas == 1 ? 2 * kMostX + kMostSums : kMostX + kMostSums;
+  const size_t smem = Room<NT>::kAll;
   e = cudaFuncSetAttribute((const void*)k_gemv<FMT, NT>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -531,35 +595,46 @@ cudaError_t resident_ctas(int ranks, int* out) {
 
 template <int FMT, int NT>
 cudaError_t launch(Params P, cudaStream_t s) {
-  constexpr int kBatch = Shape<NT>::kBatch;
+  using R = Room<NT>;
   int ranks = 1;
-  while (ranks < KQ_RANKS && P.groups / (2 * ranks) >= kBatch) ranks *= 2;
-  while (ranks < 8 && P.groups / ranks > 128) ranks *= 2;
+  while (ranks < KQ_RANKS && P.groups / (2 * ranks) >= kStep) ranks *= 2;
+  while (ranks < 8 && P.groups > ranks * R::kGroups) ranks *= 2;
   P.ranks = ranks;
   for (P.rank_shift = 0; 1 << P.rank_shift < ranks;) ++P.rank_shift;
   int ctas = 0;
   cudaError_t e = resident_ctas<FMT, NT>(ranks, &ctas);
   if (e != cudaSuccess) return e;
   const int64_t all = (P.n + 15) / 16;
-  // x of a CTA's groups in one piece where 64 KB (128 KB for one CTA an SM) hold it
+  // x of a CTA's groups in one piece where there is room
   const int mine = (P.groups + ranks - 1) / ranks;
-  P.parts = (mine + kBatch - 1) / kBatch;
-  P.seg = P.parts * kBatch;
-  const int most = 131072 / Shape<NT>::kCtas / (2048 * NT);
-  if (P.seg > most) P.seg = most;
-  // the scales of kBatch groups are one aligned load where every range and row
-  // begins at a multiple of kBatch groups
-  P.wide = P.groups % (kBatch * ranks) == 0 &&
-           (reinterpret_cast<uintptr_t>(P.scales) | reinterpret_cast<uintptr_t>(P.zeros)) %
-                   (2 * kBatch) == 0;
-  // rows for one round of CTAs, as far as their sums fit 32 KB
+  P.seg = (mine + kStep - 1) / kStep * kStep;
+  if (P.seg > R::kGroups) P.seg = R::kGroups;
+  P.recip = (65536u + P.m - 1) / P.m;
+  // a step's scales of a row are one or two aligned copies where every range and
+  // row begins at a multiple of kStep groups
+  const uintptr_t at = reinterpret_cast<uintptr_t>(P.scales) | reinterpret_cast<uintptr_t>(P.zeros);
+  P.wide = P.groups % (kStep * ranks) == 0 && P.k % 128 == 0 &&
+           at % (FMT == KQ_FMT_INT4_ASYM ? 4 : FMT == KQ_FMT_NVFP4 ? 16 : 8) == 0;
+  // rows for one round of CTAs, as far as their sums fit
   int64_t tiles = (all + ctas / ranks - 1) / (ctas / ranks);
-  const int64_t cap = kMostSums / ((int64_t)P.parts * P.m * 64);
-  if (tiles > cap) tiles = cap;
+  const int64_t room = R::kSums / (P.m * 64);           // tiles times parts, and a rank's rounding
+  if (tiles > room - ranks + 1) tiles = room - ranks + 1;
   P.tiles = (int)(tiles < 1 ? 1 : tiles);
-  const int own = (P.tiles + ranks - 1) / ranks;
-  const size_t smem = (size_t)P.seg * NT * (2048 + 64) +
+  // parts: the shortest way through the units for the CTA's warps
+  const int steps = P.seg / kStep, own = (P.tiles + ranks - 1) / ranks;
+  P.parts = 1;
+  int best = 1 << 30;
+  for (int p = 1; p <= steps && p * own * ranks <= room; ++p) {
+    const int rounds = (P.tiles * p + Shape<NT>::kWarps - 1) / Shape<NT>::kWarps;
+    const int way = rounds * ((steps + p - 1) / p);
+    if (way < best) {
+      best = way;
+      P.parts = p;
+    }
+  }
+  const size_t smem = R::kRings + (size_t)P.seg * NT * (2048 + 64) +
                       sizeof(float) * ranks * P.parts * own * 16 * P.m;
+  if (smem > (size_t)R::kAll) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((all + P.tiles - 1) / P.tiles * ranks));
   cfg.blockDim = dim3(Shape<NT>::kThreads);
@@ -588,7 +663,7 @@ cudaError_t launch_gemv(int fmt, const void* x, int x_bf16, int m, const uint8_t
                         const void* scales, const void* zeros, const float* tscale, int64_t n,
                         int k, void* y, int y_bf16, cudaStream_t s) {
   const gv::Params P{x, codes, scales, static_cast<const uint16_t*>(zeros), tscale, y, n, m, k,
-                     (k + 127) / 128, x_bf16, y_bf16, 0, 0, 0, 1, 0, 0};
+                     (k + 127) / 128, x_bf16, y_bf16, 0, 0, 0, 1, 0, 0, 0};
   switch (fmt) {
     case KQ_FMT_INT4_SYM: return gv::launch_tiles<KQ_FMT_INT4_SYM>(P, s);
     case KQ_FMT_INT4_ASYM: return gv::launch_tiles<KQ_FMT_INT4_ASYM>(P, s);
