@@ -405,6 +405,10 @@ KQ_API kq_status kq_attn_decode_int4_kv(
   if (!attn_heads_ok(batch, q_heads, kv_heads) || page_size > 65536 ||
       num_slots >= (int64_t(1) << 31) || table_width >= kMost || batch * table_width >= kMost)
     return KQ_ERR_UNSUPPORTED;
+  // the tiles a CTA walks are counted in 32 bits
+  const int64_t longest = table_width * page_size < (int64_t(1) << 31) ? table_width * page_size
+                                                                       : int64_t(1) << 31;
+  if (batch * longest >= (int64_t(1) << 42) / q_heads) return KQ_ERR_UNSUPPORTED;
   if (batch > 0) {
     if (!q || !out || !seq_lens || !workspace ||
         ws_bytes < kq::attn_workspace_bytes(batch, q_heads, kv_heads))

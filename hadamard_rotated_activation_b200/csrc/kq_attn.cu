@@ -36,6 +36,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "kq_internal.h"
@@ -54,6 +55,9 @@ constexpr int kSlack = 6;
 constexpr int kCols = 8;                      // query heads a unit carries
 constexpr int kMaxCtas = 320;
 constexpr int kMinTiles = 2;                  // tiles a CTA takes at least
+// What beginning a unit costs, in tiles: the query's rotation and the end of the
+// unit before it.  The tiles are dealt with so many more in front of each unit.
+constexpr int kUnitCost = 2;
 constexpr int kPartFloats = kCols * 128 + 2 * kCols;   // o, m, l of one head
 
 // Tokens of one sequence: positions v < vis, v + skip from `sinks` on.
@@ -106,29 +110,39 @@ __device__ __forceinline__ int cta_of(const Deal& d, int64_t tile) {
                        : d.more + (int)div64(tile - longer, d.each);
 }
 
-// A walk over a CTA's tiles: unit (b, sub) and tile within it.
+// A walk over a CTA's tiles: sequence, block of heads, chunk of query heads, tile;
+// `left` tiles remain for the CTA (units still to begin cost kUnitCost of them).
 struct Walk {
   int64_t b;
-  int sub, tile, tiles;
+  int hb, chunk, tile, tiles, left;
   Seq seq;
 };
 template <int TILE>
-__device__ __forceinline__ void next_sequence(const AttnArgs& P, int most, Walk& w) {
+__device__ __forceinline__ void step(const AttnArgs& P, int most, int blocks, int chunks, Walk& w) {
+  --w.left;
+  if (++w.tile < w.tiles) return;
+  w.left -= kUnitCost;
+  if (w.left <= 0) return;
+  w.tile = 0;
+  if (++w.chunk < chunks) return;
+  w.chunk = 0;
+  if (++w.hb < blocks) return;
+  w.hb = 0;
   do {
     ++w.b;
     w.seq = sequence(P, most, w.b);
     w.tiles = (w.seq.vis + TILE - 1) / TILE;
   } while (w.tiles == 0);
 }
-// Tiles of sequence b0 + lane (0 behind the last one) and their inclusive sum
-// over the lanes (at most 2^26 tiles a sequence).
+// What a unit of sequence b0 + lane costs, in tiles (0 behind the last one and for
+// an empty one), and the inclusive sum over the lanes (at most 2^26 a sequence).
 template <int TILE>
 __device__ __forceinline__ void scan32(const AttnArgs& P, int most, int64_t b0, Seq& seq,
                                        uint32_t& n, uint32_t& incl) {
   const int lane = threadIdx.x & 31;
   seq = Seq{0, 0};
   if (b0 + lane < P.batch) seq = sequence(P, most, b0 + lane);
-  n = incl = (uint32_t)(seq.vis + TILE - 1) / TILE;
+  n = incl = seq.vis > 0 ? (uint32_t)(seq.vis + TILE - 1) / TILE + kUnitCost : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -137,10 +151,10 @@ __device__ __forceinline__ void scan32(const AttnArgs& P, int most, int64_t b0, 
 }
 // Deals the tiles and starts the CTA's walk; false when nothing is left for it.
 template <int TILE>
-__device__ __forceinline__ bool begin(const AttnArgs& P, int most, int subs, Walk& w,
-                                      int64_t& count) {
+__device__ __forceinline__ bool begin(const AttnArgs& P, int most, int blocks, int chunks, Walk& w) {
   Seq seq;
   uint32_t n, incl;
+  const int subs = blocks * chunks;
   scan32<TILE>(P, most, 0, seq, n, incl);
   int64_t total = __shfl_sync(0xffffffffu, incl, 31);
   for (int64_t b0 = 32; b0 < P.batch; b0 += 32) {
@@ -154,22 +168,29 @@ __device__ __forceinline__ bool begin(const AttnArgs& P, int most, int subs, Wal
   const Deal dl = deal(total, gridDim.x);
   if ((int)blockIdx.x >= dl.ctas) return false;
   const int64_t first = cta_first(dl, blockIdx.x);
-  count = cta_first(dl, blockIdx.x + 1) - first;
+  w.left = (int)(cta_first(dl, blockIdx.x + 1) - first);
   int64_t base = 0;
   for (int64_t b0 = 0; b0 < P.batch; b0 += 32) {
     if (b0 > 0) scan32<TILE>(P, most, b0, seq, n, incl);
     const unsigned hit = __ballot_sync(0xffffffffu, (base + incl) * subs > first);
     if (hit) {
       const int l = __ffs(hit) - 1;
+      const int cost = (int)__shfl_sync(0xffffffffu, n, l);
       w.b = b0 + l;
       w.seq.vis = __shfl_sync(0xffffffffu, seq.vis, l);
       w.seq.skip = __shfl_sync(0xffffffffu, seq.skip, l);
-      w.tiles = (int)__shfl_sync(0xffffffffu, n, l);
-      const int64_t before = base + __shfl_sync(0xffffffffu, incl, l) - w.tiles;
+      w.tiles = cost - kUnitCost;
+      const int64_t before = base + __shfl_sync(0xffffffffu, incl, l) - cost;
       const int64_t off = first - before * subs;
-      w.sub = (int)div64(off, w.tiles);
-      w.tile = (int)(off - (int64_t)w.sub * w.tiles);
-      return true;
+      const int sub = (int)div64(off, cost);
+      w.hb = sub / chunks;
+      w.chunk = sub - w.hb * chunks;
+      w.tile = (int)(off - (int64_t)sub * cost) - kUnitCost;
+      if (w.tile < 0) {                  // the range begins in front of the unit
+        w.left += w.tile;
+        w.tile = 0;
+      }
+      return w.left > 0;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
@@ -210,15 +231,15 @@ struct Shape {
   static constexpr int kTile = kTok * kSplit;            // tokens a tile
   static constexpr int kRow = HB * 64 + 32;              // bytes a staged code row
   static constexpr int kCodes = kTile * kRow;            // keys or values of a tile
-  // per token and head the halves (sk, zk, sv, unused), then the value zero
-  // points in the order of the mma's operand, then a byte a token: not visible
-  static constexpr int kScales = HB * kTile * 8;
-  static constexpr int kZeros = HB * kTile * 2;
+  // [4][kTile][HB] halves: key scales and zero points, value scales and zero
+  // points; then a byte a token: not visible
+  static constexpr int kArray = kTile * HB * 2;
+  static constexpr int kScales = 4 * kArray;
   static constexpr int kMask = kTile;
   static constexpr int kLanes = HB == 1 ? 4 : 8;         // lanes that copy a row
   static constexpr int kPass = 32 / kLanes;              // rows a warp copies at a time
   static constexpr int kPasses = kTile / kWarps / kPass;
-  static constexpr int kStage = 2 * kCodes + kScales + kZeros + kMask;
+  static constexpr int kStage = 2 * kCodes + kScales + kMask;
   static constexpr int kStages = HB == 8 ? 3 : HB == 1 ? 3 : 2;
   // the warps of a head are joined two by two: one writes, one adds
   static constexpr int kJoin = kSplit > 1 ? kWarps / 2 * kPartFloats * 4 : 0;
@@ -230,6 +251,16 @@ template <int OFFSET>
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
   asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;"
                :: "r"(dst), "l"(src), "n"(OFFSET) : "memory");
+}
+// BYTES, or zeros (and no read).
+template <int BYTES>
+__device__ __forceinline__ void copy_or_zero(uint32_t dst, const void* src, bool in) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;"
+                 :: "r"(dst), "l"(src), "n"(BYTES), "r"(in ? BYTES : 0) : "memory");
 }
 // Every 128th byte's 16 of a row of HB heads (64 bytes a head).
 template <int HB>
@@ -296,12 +327,9 @@ __device__ __forceinline__ void hadamard_rows(float (&v)[16]) {
       }
 #pragma unroll
   for (int st = 4; st < 32; st <<= 1) {
-    const bool up = (threadIdx.x & st) != 0;
+    const float own = (threadIdx.x & st) ? -1.0f : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float o = __shfl_xor_sync(0xffffffffu, v[i], st);
-      v[i] = up ? o - v[i] : v[i] + o;
-    }
+    for (int i = 0; i < 16; ++i) v[i] = fmaf(own, v[i], __shfl_xor_sync(0xffffffffu, v[i], st));
   }
 }
 // Rotates 16 values a lane back, applies the signs and stores them as bf16.
@@ -344,10 +372,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int most = longest(P);
   const int group = P.q_heads / P.kv_heads, chunks = (group + kCols - 1) / kCols;
-  const int subs = P.kv_heads / HB * chunks;
+  const int blocks = P.kv_heads / HB;
   Walk w;
-  int64_t count = 0;
-  const bool any = begin<TILE>(P, most, subs, w, count);
+  const bool any = begin<TILE>(P, most, blocks, chunks, w);
   // sequences without a visible token have no tile: their rows are zeros
   for (int64_t b = blockIdx.x; b < P.batch; b += gridDim.x)
     if (sequence(P, most, b).vis == 0)
@@ -355,100 +382,70 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
         reinterpret_cast<uint4*>(P.out)[b * P.q_heads * 16 + i] = make_uint4(0, 0, 0, 0);
   if (!any) return;
 
-  auto step = [&](Walk& x) {
-    if (++x.tile == x.tiles) {
-      x.tile = 0;
-      if (++x.sub == subs) {
-        x.sub = 0;
-        next_sequence<TILE>(P, most, x);
-      }
-    }
-  };
-
   // ================= filling the stages.  A warp copies kTile / 8 rows, 8 lanes a
   // row (4 when a row is one head), a lane 16 bytes of each of the row's 128-byte
   // lines: the copies of a row differ by constants alone, and every request is a
   // whole line.  A token that is not visible gets the codes of row 0 (any codes
-  // do: its weight is zero).  The first four lanes of a row also load its scales
-  // and zero points, an array each, which go through registers into the stage one
-  // tile later.  Pages are looked up one tile ahead.
+  // do: its weight is zero).  The first four lanes of a row also copy its scales
+  // and zero points, an array each (2 bytes, where a row is one head, are too few
+  // for an asynchronous copy and go through a register into the stage one tile
+  // later).  Pages are looked up one tile ahead.
   const int arr = lane % S::kLanes;
   const uint16_t* sc_from = arr == 0 ? P.k_scales : arr == 1 ? P.k_zeros
                             : arr == 2 ? P.v_scales : P.v_zeros;
   const int my_row = warp * (TILE / kWarps) + lane / S::kLanes;    // + pass * kPass
+  const uint32_t my_codes = smem_u32(smem) + (uint32_t)my_row * S::kRow + 16 * arr;
+  const uint32_t my_scales = smem_u32(smem) + 2 * S::kCodes + arr * S::kArray + my_row * HB * 2;
   Walk ahead = w;
-  int64_t fetched = 0;                    // tiles whose copies were issued
-  int fill = 0, late = -1;                // stage to fill; stage whose scales are still in registers
+  int fill = 0;                           // stage to fill
+  [[maybe_unused]] int late = -1;         // stage whose scales are still in registers
+  [[maybe_unused]] uint16_t sreg[S::kPasses];
   Place at[S::kPasses];
-  uint16_t sreg[S::kPasses][HB];
-  bool gone[S::kPasses];
   auto look = [&] {
 #pragma unroll
     for (int j = 0; j < S::kPasses; ++j)
       at[j] = place(P, pages, ahead, ahead.tile * TILE + my_row + j * S::kPass);
   };
   auto store_scales = [&] {
-    if (late < 0) return;
-    uint8_t* base = smem + late * S::kStage + 2 * S::kCodes;
+    if constexpr (HB == 1) {
+      if (late < 0) return;
 #pragma unroll
-    for (int j = 0; j < S::kPasses; ++j) {
-      const int tok = my_row + j * S::kPass, r16 = tok & 15, r8 = tok & 7;
-      // the mma's operand order: rows 2t and 2t + 1 of an accumulator are tokens t
-      // and 4 + (t + 2) % 4
-      const int zt = r8 < 4 ? r8 : (r8 + 2) & 3;
-      const int zpos = (tok >> 4) * 16 + zt * 4 + (r16 >> 3) * 2 + (r8 >> 2);
-      uint16_t* to = arr < 3 ? reinterpret_cast<uint16_t*>(base) + tok * 4 + arr
-                             : reinterpret_cast<uint16_t*>(base + S::kScales) + zpos;
-      const int pitch = arr < 3 ? TILE * 4 : TILE;
-      if (arr < 4) {
-#pragma unroll
-        for (int h = 0; h < HB; ++h) to[h * pitch] = sreg[j][h];
-      }
-      if (arr == 0) base[S::kScales + S::kZeros + tok] = gone[j];
+      for (int j = 0; j < S::kPasses; ++j)
+        *reinterpret_cast<uint16_t*>(smem + late * S::kStage + 2 * S::kCodes + arr * S::kArray +
+                                     (my_row + j * S::kPass) * 2) = sreg[j];
+      late = -1;
     }
-    late = -1;
   };
   auto fetch = [&] {
-    if (fetched < count) {
-      const int64_t head0 = (int64_t)(ahead.sub / chunks) * HB;
+    if (ahead.left > 0) {
+      const int head0 = ahead.hb * HB;
+      const uint32_t base = fill * S::kStage;
 #pragma unroll
       for (int j = 0; j < S::kPasses; ++j) {
         const int r = cache_row(P, at[j]);
         const int64_t row = (int64_t)max(r, 0) * P.kv_heads + head0;
         const int64_t off = row * 64 + 16 * arr;
-        const uint32_t to = smem_u32(smem) + fill * S::kStage +
-                            (uint32_t)(my_row + j * S::kPass) * S::kRow + 16 * arr;
+        const uint32_t to = my_codes + base + j * S::kPass * S::kRow;
         copy_lines<HB>(to, P.k_codes + off);
         copy_lines<HB>(to + S::kCodes, P.v_codes + off);
-        gone[j] = r < 0;
-#pragma unroll
-        for (int h = 0; h < HB; ++h) sreg[j][h] = 0;
-        if (r >= 0 && arr < 4) {
-          if constexpr (HB == 8)
-            *reinterpret_cast<uint4*>(sreg[j]) = __ldg(reinterpret_cast<const uint4*>(sc_from + row));
-          else if constexpr (HB == 4)
-            *reinterpret_cast<uint2*>(sreg[j]) = __ldg(reinterpret_cast<const uint2*>(sc_from + row));
-          else if constexpr (HB == 2)
-            *reinterpret_cast<uint32_t*>(sreg[j]) =
-                __ldg(reinterpret_cast<const uint32_t*>(sc_from + row));
-          else
-            sreg[j][0] = __ldg(sc_from + row);
+        if constexpr (HB == 1) {
+          sreg[j] = r >= 0 ? __ldg(sc_from + row) : 0;
+        } else {
+          if (arr < 4)
+            copy_or_zero<2 * HB>(my_scales + base + j * S::kPass * HB * 2, sc_from + row, r >= 0);
         }
+        if (arr == 0) smem[base + 2 * S::kCodes + S::kScales + my_row + j * S::kPass] = r < 0;
       }
       late = fill;
       if (++fill == S::kStages) fill = 0;
-      if (++fetched < count) {
-        step(ahead);
-        look();
-      }
+      step<TILE>(P, most, blocks, chunks, ahead);
+      if (ahead.left > 0) look();
     }
     commit_copies();
   };
   look();
 #pragma unroll 1
   for (int i = 0; i + 1 < S::kStages; ++i) {
-
-
     store_scales();
     fetch();
   }
@@ -467,45 +464,39 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
     float m[2], ref[2], l[2], zs[4], o[8][4];
     int ev = 0;
     bool fresh = false;                    // no tile of the unit seen yet
-    int64_t it = 0;
     int segment = 0;
-    while (it < count) {
+    while (w.left > 0) {
       // ---- the unit's query, rotated; lane (g, t) holds dimensions 32 t .. of column g
-      const int kh = w.sub / chunks * HB + hw;
-      const int col0 = w.sub % chunks * kCols;
+      const int kh = w.hb * HB + hw;
+      const int col0 = w.chunk * kCols;
       const int columns = min(kCols, group - col0);
       {
         float q[32];
-        if (g < columns) {
+        {
           const uint4* from = reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(P.q) +
-              (w.b * P.q_heads + (int64_t)kh * group + col0 + g) * 128 + 32 * t);
+              (w.b * P.q_heads + (int64_t)kh * group + col0 + min(g, columns - 1)) * 128 + 32 * t);
+          const uint4* sp = reinterpret_cast<const uint4*>(P.k_signs + kh * 128 + 32 * t);
+          uint4 v[4], sg[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 v = __ldg(from + i);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              q[8 * i + 2 * j] = __uint_as_float(x[j] << 16);
-              q[8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
-            }
-          }
+          for (int i = 0; i < 4; ++i) v[i] = __ldg(from + i);
           if (P.k_signs) {
-            const uint4* sp = reinterpret_cast<const uint4*>(P.k_signs + kh * 128 + 32 * t);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint4 v = __ldg(sp + i);
-              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const uint32_t neg = x[j >> 2] << (24 - 8 * (j & 3)) & 0x80000000u;
-                q[16 * i + j] = __uint_as_float(__float_as_uint(q[16 * i + j]) ^ neg);
-              }
-            }
+            sg[0] = __ldg(sp);
+            sg[1] = __ldg(sp + 1);
           }
-        } else {
+          const uint32_t ok = g < columns ? 0xffffffffu : 0u;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) q[i] = 0.0f;
+          for (int i = 0; i < 16; ++i) {
+            const uint4 x4 = v[i >> 2], s4 = sg[i >> 3];
+            const uint32_t x = (i & 3) == 0 ? x4.x : (i & 3) == 1 ? x4.y : (i & 3) == 2 ? x4.z : x4.w;
+            const uint32_t c = (i >> 1 & 3) == 0 ? s4.x : (i >> 1 & 3) == 1 ? s4.y
+                               : (i >> 1 & 3) == 2 ? s4.z : s4.w;
+            // the sign bytes' top bits onto those of the two bf16 values
+            const uint32_t flip = __byte_perm(c, 0, i & 1 ? 0x3424 : 0x1404) & 0x80008000u;
+            const uint32_t y = (x ^ flip) & ok;
+            q[2 * i] = __uint_as_float(y << 16);
+            q[2 * i + 1] = __uint_as_float(y & 0xffff0000u);
+          }
         }
 #pragma unroll
         for (int st = 1; st < 32; st <<= 1)
@@ -518,14 +509,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
             }
         float top = 0.0f;
 #pragma unroll
-        for (int st = 1; st < 4; st <<= 1)
+        for (int st = 1; st < 4; st <<= 1) {
+          const float own = (lane & st) ? -1.0f : 1.0f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float v = __shfl_xor_sync(0xffffffffu, q[i], st);
-            q[i] = (lane & st) ? v - q[i] : q[i] + v;
-          }
+          for (int i = 0; i < 32; ++i)
+            q[i] = fmaf(own, q[i], __shfl_xor_sync(0xffffffffu, q[i], st));
+        }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(q[i]));
+        for (int i = 0; i < 32; i += 2) top = fmax3(top, fabsf(q[i]), fabsf(q[i + 1]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // fp16 with a power of two per column that puts its largest element in
@@ -569,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
         ev = -14;
         fresh = true;
       }
-      const int64_t todo = min((int64_t)(w.tiles - w.tile), count - it);
-      for (int64_t end = it + todo; it < end; ++it) {
+      const int todo = min(w.tiles - w.tile, w.left);
+      for (int it = 0; it < todo; ++it) {
         // the tile's copies have landed and its scales are stored, and every warp
         // is done with the stage that is filled next
         wait_copies<S::kStages - 2>();
@@ -581,14 +572,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
         if (++stage == S::kStages) stage = 0;
         const uint8_t* kb = smem + s * S::kStage + tok0 * S::kRow + hw * 64;
         const uint8_t* vb = kb + S::kCodes;
-        const uint2* sb = reinterpret_cast<const uint2*>(smem + s * S::kStage + 2 * S::kCodes) +
-                          hw * TILE + tok0;
-        const uint2* zb = reinterpret_cast<const uint2*>(smem + s * S::kStage + 2 * S::kCodes +
-                                                         S::kScales) +
-                          (hw * TILE + tok0) / 4 + t;
-        const uint32_t hidden = __ballot_sync(
-            0xffffffffu, smem[s * S::kStage + 2 * S::kCodes + S::kScales + S::kZeros + tok0 +
-                              lane % S::kTok]);
+        const uint8_t* scales = smem + s * S::kStage + 2 * S::kCodes;
+        const uint16_t* sb = reinterpret_cast<const uint16_t*>(scales) + tok0 * HB + hw;
+        const uint32_t hidden =
+            __ballot_sync(0xffffffffu, scales[S::kScales + tok0 + lane % S::kTok]);
         float sc[MB][2][2];                // [block][row g or g + 8][column], minus ref
         float vs[MB][2];                   // value scale of the row, times 2^(15 - kSlack - ev)
         const float vup = pow2f(15 - kSlack - ev);
@@ -609,12 +596,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
           }
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const uint2 sz = sb[mb * 16 + 8 * r + mine];
-            const float2 k2 = half2_floats(sz.x);
+            const uint16_t* at = sb + (mb * 16 + 8 * r + mine) * HB;
+            const float ks = f16_bits_to_f32(at[0]);
+            const float kz = f16_bits_to_f32(at[S::kArray / 2]);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              sc[mb][r][j] = fmaf(k2.x, fmaf(fa[j], c[2 * r + j], -k2.y * fz[j]), -ref[j]);
-            vs[mb][r] = f16_bits_to_f32((uint16_t)sz.y) * vup;
+              sc[mb][r][j] = fmaf(ks, fmaf(fa[j], c[2 * r + j], -kz * fz[j]), -ref[j]);
+            vs[mb][r] = f16_bits_to_f32(at[S::kArray]) * vup;
           }
           vtop = fmax3(vtop, fabsf(vs[mb][0]), fabsf(vs[mb][1]));
         }
@@ -685,8 +673,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
           // the zero points as one more dimension (every row the same)
-          const uint2 z = zb[mb * 4];
-          mma16816(zs, z.x, z.x, z.y, z.y, pf[mb][0], pf[mb][1]);
+          const uint16_t* zv = sb + 3 * (S::kArray / 2) + mb * 16 * HB;
+          const uint32_t z01 = zv[even * HB] | (uint32_t)zv[odd * HB] << 16;
+          const uint32_t z23 = zv[(8 + even) * HB] | (uint32_t)zv[(8 + odd) * HB] << 16;
+          mma16816(zs, z01, z01, z23, z23, pf[mb][0], pf[mb][1]);
           uint2 x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -789,22 +779,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
         }
       }
       ++segment;
-      if (it < count) {
-        w.tile += (int)todo - 1;
-        step(w);
-      }
+      w.tile += todo - 1;
+      w.left -= todo - 1;
+      step<TILE>(P, most, blocks, chunks, w);
     }
   }
 }
 
 // Joins the partial sums of the units that more than one CTA worked on, in CTA
-// order.  A CTA takes one (sequence, query head): a lane holds 4 dimensions
-// and the warps share the partial sums.
+// order.  A CTA takes one (sequence, query head): a lane holds 4 dimensions and
+// the warps share the partial sums, each with a running maximum of its own, so
+// that sums and maxima are loaded at the same time.
 constexpr int kJoinWarps = 16;                // at most
 template <int HB>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) {
   constexpr int TILE = Shape<HB>::kTile;
-  __shared__ float part_m[kMaxCtas], part_l[kMaxCtas];
+  __shared__ float wm[kJoinWarps], wl[kJoinWarps];
   __shared__ __align__(16) float red[kJoinWarps][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int64_t b = blockIdx.x;
@@ -816,67 +806,90 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
   const int tiles = (sequence(P, most, b).vis + TILE - 1) / TILE;
   int64_t before = 0, all = 0;
   for (int64_t i = lane; i < P.batch; i += 32) {
-    const int n = (sequence(P, most, i).vis + TILE - 1) / TILE;
+    const int vis = sequence(P, most, i).vis;
+    const int n = vis > 0 ? (vis + TILE - 1) / TILE + kUnitCost : 0;
     all += n;
     before += i < b ? n : 0;
   }
   const Deal dl = deal(warp_sum(all) * subs, grid);
-  const int64_t u0 = warp_sum(before) * subs + (int64_t)sub * tiles;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tiles == 0) return;
-  const int c0 = cta_of(dl, u0), n = cta_of(dl, u0 + tiles - 1) - c0 + 1;
-  if (n == 1) return;
+  const int64_t u0 = warp_sum(before) * subs + (int64_t)sub * (tiles + kUnitCost);
+  const int c0 = cta_of(dl, u0 + kUnitCost);
+  const int n = tiles > 0 ? cta_of(dl, u0 + kUnitCost + tiles - 1) - c0 + 1 : 0;
   // CTA c0 has its second slot for this unit unless it begins with it
   const int second = cta_first(dl, c0) < u0 ? 1 : 0;
   const float* base = static_cast<const float*>(P.workspace) +
                       ((int64_t)c0 * 2 * kWarps + kh % HB) * kPartFloats;
-  auto slot = [&](int i) {
-    return base + (i * 2 + (i == 0 ? second : 0)) * kWarps * kPartFloats;
-  };
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const float* s = slot(i);
-    part_m[i] = s[kCols * 128 + col];
-    part_l[i] = s[kCols * 128 + kCols + col];
-  }
-  __syncthreads();
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, part_m[i]);
-  top = warp_max(top);
-  const float ref = top == -INFINITY ? 0.0f : top;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n < 2) return;
+  float m = -INFINITY, l = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-  for (int i = warp; i < n; i += warps) {
-    const float f = exp2_(part_m[i] - ref);
-    const float4 v = *reinterpret_cast<const float4*>(slot(i) + col * 128 + 4 * lane);
-    acc.x = fmaf(f, v.x, acc.x);
-    acc.y = fmaf(f, v.y, acc.y);
-    acc.z = fmaf(f, v.z, acc.z);
-    acc.w = fmaf(f, v.w, acc.w);
+  constexpr int kAhead = 4;
+  for (int i0 = warp; i0 < n; i0 += kAhead * warps) {
+    float pm[kAhead], pl[kAhead];
+    float4 v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * warps;
+      pm[k] = -INFINITY;
+      pl[k] = 0.0f;
+      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i < n) {
+        const float* s = base + (i * 2 + (i == 0 ? second : 0)) * kWarps * kPartFloats;
+        pm[k] = s[kCols * 128 + col];
+        pl[k] = s[kCols * 128 + kCols + col];
+        v[k] = *reinterpret_cast<const float4*>(s + col * 128 + 4 * lane);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) top = fmaxf(top, pm[k]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    const float keep = exp2_(m - ref);
+    m = top;
+    l *= keep;
+    acc.x *= keep;
+    acc.y *= keep;
+    acc.z *= keep;
+    acc.w *= keep;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const float f = exp2_(pm[k] - ref);
+      l = fmaf(f, pl[k], l);
+      acc.x = fmaf(f, v[k].x, acc.x);
+      acc.y = fmaf(f, v[k].y, acc.y);
+      acc.z = fmaf(f, v[k].z, acc.z);
+      acc.w = fmaf(f, v[k].w, acc.w);
+    }
   }
   *reinterpret_cast<float4*>(&red[warp][4 * lane]) = acc;
+  if (lane == 0) {
+    wm[warp] = m;
+    wl[warp] = l;
+  }
   __syncthreads();
   if (threadIdx.x < 128) {
-    float sum = 0.0f;
+    float top = -INFINITY, sum = 0.0f, ls = 0.0f;
+    for (int k = 0; k < warps; ++k) top = fmaxf(top, wm[k]);
+    const float ref = top == -INFINITY ? 0.0f : top;
 #pragma unroll 4
-    for (int k = 0; k < warps; ++k) sum += red[k][threadIdx.x];
-    red[0][threadIdx.x] = sum;
+    for (int k = 0; k < warps; ++k) {
+      const float f = exp2_(wm[k] - ref);
+      sum = fmaf(f, red[k][threadIdx.x], sum);
+      ls = fmaf(f, wl[k], ls);
+    }
+    red[0][threadIdx.x] = ls > 0.0f ? sum / ls : 0.0f;
   }
   __syncthreads();
   if (warp == 0) {
-    float l = 0.0f;
-    for (int i = lane; i < n; i += 32) l += part_l[i] * exp2_(part_m[i] - ref);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const int g = lane >> 2;
     float v[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 f = *reinterpret_cast<const float4*>(&red[0][16 * g + 4 * i]);
-      v[4 * i] = f.x * inv;
-      v[4 * i + 1] = f.y * inv;
-      v[4 * i + 2] = f.z * inv;
-      v[4 * i + 3] = f.w * inv;
+      v[4 * i] = f.x;
+      v[4 * i + 1] = f.y;
+      v[4 * i + 2] = f.z;
+      v[4 * i + 3] = f.w;
     }
     store_result(P, v, b, qh, kh, (lane & 3) == 0);
   }
@@ -884,14 +897,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
 
 template <int HB>
 cudaError_t launch(const AttnArgs& P, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute((const void*)k_attn<HB>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Shape<HB>::kSmem);
-  if (e != cudaSuccess) return e;
+  // looked up and set once a device
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
   int dev = 0, sms = 0;
-  e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= kDevices || (sms = known[dev].load(std::memory_order_relaxed)) == 0) {
+    e = cudaFuncSetAttribute((const void*)k_attn<HB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Shape<HB>::kSmem);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kDevices) known[dev].store(sms, std::memory_order_relaxed);
+  }
   const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
   PageDiv d{0, 0};
   if (P.page_size > 1) {

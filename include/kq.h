@@ -365,7 +365,8 @@ KQ_API kq_status kq_gemv(int fmt, const void* x, int x_dtype, int64_t m, const u
  * Supported: 1 <= kv_heads <= 128, q_heads a multiple of kv_heads with
  * q_heads / kv_heads <= 128, 1 <= page_size <= 65536, window and sinks >= 0,
  * softmax_scale finite, num_slots below 2^31, batch * table_width below 2^40,
- * batch <= 65535.  batch == 0 is a no-op.  The query and the softmax weights are held in
+ * batch <= 65535, batch * q_heads * min(table_width * page_size, 2^31) below 2^42.
+ * batch == 0 is a no-op.  The query and the softmax weights are held in
  * fp16 with a power-of-two scale per head (relative rounding 2^-11) for the
  * tensor cores; scores, maxima, sums and the accumulated values in fp32.
  * Results do not depend on the order of execution.
