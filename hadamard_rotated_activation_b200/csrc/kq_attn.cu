@@ -786,26 +786,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
   }
 }
 
-// Joins the partial sums of the units that more than one CTA worked on, in CTA
-// order.  A CTA takes one (sequence, query head): a lane holds 4 dimensions and
-// the warps share the partial sums, each with a running maximum of its own, so
-// that sums and maxima are loaded at the same time.
-constexpr int kJoinWarps = 16;                // at most
+// ---- joining the partial sums of the units that more than one CTA worked on, in
+// CTA order.
+constexpr int kRowWarps = 4;                  // warps with a row each, when there are many rows
+
+// Where the partial sums of a unit lie: `n` of them, from CTA c0 on.
+struct Parts {
+  const float* base;
+  int n, second;
+  __device__ __forceinline__ const float* slot(int i) const {
+    return base + (i * 2 + (i == 0 ? second : 0)) * kWarps * kPartFloats;
+  }
+};
 template <int HB>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) {
+__device__ __forceinline__ Parts parts_of(const AttnArgs& P, int grid, int64_t b, int kh, int chunk) {
   constexpr int TILE = Shape<HB>::kTile;
-  __shared__ float wm[kJoinWarps], wl[kJoinWarps];
-  __shared__ __align__(16) float red[kJoinWarps][128];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int64_t b = blockIdx.x;
-  const int qh = blockIdx.y, group = P.q_heads / P.kv_heads;
-  const int chunks = (group + kCols - 1) / kCols, kh = qh / group;
-  const int subs = P.kv_heads / HB * chunks;
-  const int sub = kh / HB * chunks + (qh - kh * group) / kCols, col = (qh - kh * group) % kCols;
+  const int chunks = (P.q_heads / P.kv_heads + kCols - 1) / kCols;
+  const int subs = P.kv_heads / HB * chunks, sub = kh / HB * chunks + chunk;
   const int most = longest(P);
   const int tiles = (sequence(P, most, b).vis + TILE - 1) / TILE;
   int64_t before = 0, all = 0;
-  for (int64_t i = lane; i < P.batch; i += 32) {
+  for (int64_t i = threadIdx.x & 31; i < P.batch; i += 32) {
     const int vis = sequence(P, most, i).vis;
     const int n = vis > 0 ? (vis + TILE - 1) / TILE + kUnitCost : 0;
     all += n;
@@ -814,65 +815,129 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
   const Deal dl = deal(warp_sum(all) * subs, grid);
   const int64_t u0 = warp_sum(before) * subs + (int64_t)sub * (tiles + kUnitCost);
   const int c0 = cta_of(dl, u0 + kUnitCost);
-  const int n = tiles > 0 ? cta_of(dl, u0 + kUnitCost + tiles - 1) - c0 + 1 : 0;
+  Parts p;
+  p.n = tiles > 0 ? cta_of(dl, u0 + kUnitCost + tiles - 1) - c0 + 1 : 0;
   // CTA c0 has its second slot for this unit unless it begins with it
-  const int second = cta_first(dl, c0) < u0 ? 1 : 0;
-  const float* base = static_cast<const float*>(P.workspace) +
-                      ((int64_t)c0 * 2 * kWarps + kh % HB) * kPartFloats;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (n < 2) return;
-  float m = -INFINITY, l = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  constexpr int kAhead = 4;
-  for (int i0 = warp; i0 < n; i0 += kAhead * warps) {
-    float pm[kAhead], pl[kAhead];
-    float4 v[kAhead];
+  p.second = cta_first(dl, c0) < u0 ? 1 : 0;
+  p.base = static_cast<const float*>(P.workspace) +
+           ((int64_t)c0 * 2 * kWarps + kh % HB) * kPartFloats;
+  return p;
+}
+
+// Maximum, sum and values (4 dimensions a lane) of column `col` over the partial
+// sums i0, i0 + by, ...; AHEAD of them are loaded at a time, with a running maximum.
+struct Joined {
+  float m, l;
+  float4 v;
+};
+template <int AHEAD>
+__device__ __forceinline__ Joined sum_parts(const Parts& p, int col, int i0, int by) {
+  const int lane = threadIdx.x & 31;
+  Joined r{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  for (; i0 < p.n; i0 += AHEAD * by) {
+    float pm[AHEAD], pl[AHEAD];
+    float4 v[AHEAD];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + k * warps;
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + k * by;
       pm[k] = -INFINITY;
       pl[k] = 0.0f;
       v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (i < n) {
-        const float* s = base + (i * 2 + (i == 0 ? second : 0)) * kWarps * kPartFloats;
+      if (i < p.n) {
+        const float* s = p.slot(i);
         pm[k] = s[kCols * 128 + col];
         pl[k] = s[kCols * 128 + kCols + col];
         v[k] = *reinterpret_cast<const float4*>(s + col * 128 + 4 * lane);
       }
     }
-    float top = m;
+    float top = r.m;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) top = fmaxf(top, pm[k]);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    const float keep = exp2_(m - ref);
-    m = top;
-    l *= keep;
-    acc.x *= keep;
-    acc.y *= keep;
-    acc.z *= keep;
-    acc.w *= keep;
+    for (int k = 0; k < AHEAD; ++k) top = fmaxf(top, pm[k]);
+    const float ref = top == -INFINITY ? 0.0f : top, keep = exp2_(r.m - ref);
+    r.m = top;
+    r.l *= keep;
+    r.v.x *= keep;
+    r.v.y *= keep;
+    r.v.z *= keep;
+    r.v.w *= keep;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
+    for (int k = 0; k < AHEAD; ++k) {
       const float f = exp2_(pm[k] - ref);
-      l = fmaf(f, pl[k], l);
-      acc.x = fmaf(f, v[k].x, acc.x);
-      acc.y = fmaf(f, v[k].y, acc.y);
-      acc.z = fmaf(f, v[k].z, acc.z);
-      acc.w = fmaf(f, v[k].w, acc.w);
+      r.l = fmaf(f, pl[k], r.l);
+      r.v.x = fmaf(f, v[k].x, r.v.x);
+      r.v.y = fmaf(f, v[k].y, r.v.y);
+      r.v.z = fmaf(f, v[k].z, r.v.z);
+      r.v.w = fmaf(f, v[k].w, r.v.w);
     }
   }
-  *reinterpret_cast<float4*>(&red[warp][4 * lane]) = acc;
+  return r;
+}
+// A warp stores the row whose 128 values lie in shared memory.
+__device__ __forceinline__ void store_row(const AttnArgs& P, const float* row, int64_t b, int qh,
+                                          int kh) {
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 f = *reinterpret_cast<const float4*>(row + 16 * g + 4 * i);
+    v[4 * i] = f.x;
+    v[4 * i + 1] = f.y;
+    v[4 * i + 2] = f.z;
+    v[4 * i + 3] = f.w;
+  }
+  store_result(P, v, b, qh, kh, (lane & 3) == 0);
+}
+
+// Many rows: a CTA takes (sequence, cached head, chunk of its query heads), a warp
+// a query head at a time.
+template <int HB>
+__global__ void __launch_bounds__(32 * kRowWarps) k_join_rows(AttnArgs P, int grid) {
+  __shared__ __align__(16) float rows[kRowWarps][128];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = P.q_heads / P.kv_heads, chunks = (group + kCols - 1) / kCols;
+  const int64_t b = blockIdx.x;
+  const int kh = blockIdx.y / chunks, chunk = blockIdx.y - kh * chunks;
+  const Parts p = parts_of<HB>(P, grid, b, kh, chunk);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.n < 2) return;
+  const int columns = min(kCols, group - chunk * kCols);
+  for (int col = warp; col < columns; col += kRowWarps) {
+    const Joined r = sum_parts<8>(p, col, 0, 1);
+    const float inv = r.l > 0.0f ? 1.0f / r.l : 0.0f;
+    __syncwarp();
+    *reinterpret_cast<float4*>(&rows[warp][4 * lane]) =
+        make_float4(r.v.x * inv, r.v.y * inv, r.v.z * inv, r.v.w * inv);
+    __syncwarp();
+    store_row(P, rows[warp], b, kh * group + chunk * kCols + col, kh);
+  }
+}
+
+// Fewer rows, which may have partial sums of many CTAs: a CTA takes one.
+template <int HB, int kJoinWarps>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join_wide(AttnArgs P, int grid) {
+  __shared__ float wm[kJoinWarps], wl[kJoinWarps];
+  __shared__ __align__(16) float red[kJoinWarps][128];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t b = blockIdx.x;
+  const int qh = blockIdx.y, group = P.q_heads / P.kv_heads, kh = qh / group;
+  const int chunk = (qh - kh * group) / kCols, col = (qh - kh * group) % kCols;
+  const Parts p = parts_of<HB>(P, grid, b, kh, chunk);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.n < 2) return;
+  const Joined r = sum_parts<4>(p, col, warp, kJoinWarps);
+  *reinterpret_cast<float4*>(&red[warp][4 * lane]) = r.v;
   if (lane == 0) {
-    wm[warp] = m;
-    wl[warp] = l;
+    wm[warp] = r.m;
+    wl[warp] = r.l;
   }
   __syncthreads();
   if (threadIdx.x < 128) {
     float top = -INFINITY, sum = 0.0f, ls = 0.0f;
-    for (int k = 0; k < warps; ++k) top = fmaxf(top, wm[k]);
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, wm[k]);
     const float ref = top == -INFINITY ? 0.0f : top;
-#pragma unroll 4
-    for (int k = 0; k < warps; ++k) {
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) {
       const float f = exp2_(wm[k] - ref);
       sum = fmaf(f, red[k][threadIdx.x], sum);
       ls = fmaf(f, wl[k], ls);
@@ -880,19 +945,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(AttnArgs P, int grid) 
     red[0][threadIdx.x] = ls > 0.0f ? sum / ls : 0.0f;
   }
   __syncthreads();
-  if (warp == 0) {
-    const int g = lane >> 2;
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = *reinterpret_cast<const float4*>(&red[0][16 * g + 4 * i]);
-      v[4 * i] = f.x;
-      v[4 * i + 1] = f.y;
-      v[4 * i + 2] = f.z;
-      v[4 * i + 3] = f.w;
-    }
-    store_result(P, v, b, qh, kh, (lane & 3) == 0);
-  }
+  if (warp == 0) store_row(P, red[0], b, qh, kh);
 }
 
 template <int HB>
@@ -922,16 +975,29 @@ cudaError_t launch(const AttnArgs& P, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)P.batch, (unsigned)P.q_heads);
-  // few rows: more warps to each, they may have partial sums of every CTA
-  cfg.blockDim = dim3(P.batch * P.q_heads <= 2 * sms ? 32 * kJoinWarps : 128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_join<HB>, P, grid);
+  // A row's CTA of 16 warps, 4 or 1, as far as they all run at a time: 32
+  // sequences of 32 heads (1024 rows) took 24.4 us with 4 warps and 25.5 with 1,
+  // 2048 rows 31.0 with 4 and 28.1 with 1.
+  const int64_t rows = P.batch * P.q_heads;
+  cfg.gridDim = dim3((unsigned)P.batch, (unsigned)P.q_heads);
+  if (rows <= 2 * sms) {
+    cfg.blockDim = dim3(32 * 16);
+    return cudaLaunchKernelEx(&cfg, k_join_wide<HB, 16>, P, grid);
+  }
+  if (rows <= 8 * sms) {
+    cfg.blockDim = dim3(32 * 4);
+    return cudaLaunchKernelEx(&cfg, k_join_wide<HB, 4>, P, grid);
+  }
+  const int chunks = (P.q_heads / P.kv_heads + kCols - 1) / kCols;
+  cfg.gridDim = dim3((unsigned)P.batch, (unsigned)(P.kv_heads * chunks));
+  cfg.blockDim = dim3(32 * kRowWarps);
+  return cudaLaunchKernelEx(&cfg, k_join_rows<HB>, P, grid);
 }
 
 }  // namespace at
