@@ -276,9 +276,15 @@ def nvfp4_dynamic_sharded(x, block: int, signs, codes, block_scales, tensor_scal
                              all_reduce_max, x.shape[0] == 0)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def kq_gemm_nvfp4(a_codes, a_scales, a_tensor_scale, b_codes, b_scales, b_tensor_scale, c,
@@ -295,31 +301,40 @@ def kq_gemm_nvfp4(a_codes, a_scales, a_tensor_scale, b_codes, b_scales, b_tensor
 
 
 # ------------------------------------------------- decode-step operators
-def _want(t, what: str, dtype, shape, device=None) -> int:
-    """Device pointer of a contiguous CUDA tensor of this type and shape (on
-    this device); ValueError for anything else.  The kernels take sizes from
-    the shapes, so a wrong one would read or write out of bounds."""
+# These calls are short (a few microseconds of GPU work), so their marshalling
+# asks each tensor only what the kernels rely on.
+def _want(t, what: str, dtype, shape, index: int) -> int:
+    """Device pointer of a contiguous tensor of this type and shape on device
+    `index`; ValueError for anything else.  The kernels take sizes from the
+    shapes, so a wrong one would read or write out of bounds."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 \
+            and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{what}: kq functions take CUDA tensors (device pointers)")
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what}: expected {dtype} {list(shape)}, "
                          f"got {t.dtype} {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: kq functions take contiguous tensors")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what}: on {t.device}, the call's tensors are on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{what}: on cuda:{t.get_device()}, the call's tensors are on cuda:{index}")
 
 
-def _launch(fn, where: str, device, stream, *args) -> None:
-    """fn(*args, stream) with `device` current; its current stream when none is
-    given."""
-    cuda = _torch().cuda
-    if cuda.current_device() != device.index:
-        with cuda.device(device):
-            _check(fn(*args, _stream(stream)), where)
+def _launch(fn, where: str, index: int, stream, *args) -> None:
+    """fn(*args, stream) with device `index` current; its current stream when
+    none is given."""
+    torch = _torch()
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, stream)
     else:
-        _check(fn(*args, _stream(stream)), where)
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != KQ_OK:
+        raise KQError(status, where)
 
 
 def kq_gemv(fmt: int, x, codes, scales, zeros, tensor_scale, group: int, y,
@@ -329,23 +344,22 @@ def kq_gemv(fmt: int, x, codes, scales, zeros, tensor_scale, group: int, y,
     torch = _torch()
     if x.dim() != 2 or codes.dim() != 2:
         raise ValueError("x is [m, k] and codes are [n, k/2]")
-    (m, k), n, dev = x.shape, codes.shape[0], x.device
-    if fmt == KQ_FMT_INT4_SYM:
-        kind, shape = torch.float32, (n,)
-    elif fmt == KQ_FMT_INT4_ASYM:
-        kind, shape = torch.float16, (n, k // 128)
+    (m, k), n, at = x.shape, codes.shape[0], x.get_device()
+    z = t = None
+    if fmt == KQ_FMT_INT4_ASYM:
+        s = _want(scales, "scales", torch.float16, (n, k // 128), at)
+        z = _want(zeros, "zeros", torch.float16, (n, k // 128), at)
+    elif fmt == KQ_FMT_INT4_SYM:
+        s = _want(scales, "scales", torch.float32, (n,), at)
     elif fmt == KQ_FMT_NVFP4:
-        kind, shape = torch.uint8, (n, k // 16)
+        s = _want(scales, "scales", torch.uint8, (n, k // 16), at)
+        t = _want(tensor_scale, "tensor_scale", torch.float32, (1,), at)
     else:
-        kind, shape = torch.uint8, (n, k // 32)
-    asym, nv = fmt == KQ_FMT_INT4_ASYM, fmt == KQ_FMT_NVFP4
-    _launch(lib().kq_gemv, "kq_gemv", dev, stream, fmt,
-            _want(x, "x", x.dtype, (m, k)), _dtype_code(x), m,
-            _want(codes, "codes", torch.uint8, (n, k // 2), dev),
-            _want(scales, "scales", kind, shape, dev),
-            _want(zeros, "zeros", kind, shape, dev) if asym else None,
-            _want(tensor_scale, "tensor_scale", torch.float32, (1,), dev) if nv else None,
-            n, k, group, _want(y, "y", y.dtype, (m, n), dev), _dtype_code(y))
+        s = _want(scales, "scales", torch.uint8, (n, k // 32), at)
+    _launch((_lib or lib()).kq_gemv, "kq_gemv", at, stream, fmt,
+            _want(x, "x", x.dtype, (m, k), at), _dtype_code(x), m,
+            _want(codes, "codes", torch.uint8, (n, k // 2), at), s, z, t, n, k, group,
+            _want(y, "y", y.dtype, (m, n), at), _dtype_code(y))
 
 
 class KVCacheInt4:
@@ -354,22 +368,22 @@ class KVCacheInt4:
     and zeros fp16 [num_slots, dim/128]; with one more leading dimension a
     cache of several layers.  A view of the caller's tensors, checked once."""
 
-    __slots__ = ("codes", "scales", "zeros", "layers", "num_slots", "dim", "device", "layered")
+    __slots__ = ("codes", "scales", "zeros", "layers", "num_slots", "dim", "index", "layered")
 
     def __init__(self, codes, scales, zeros):
         torch = _torch()
         if codes.dim() not in (2, 3):
             raise ValueError("codes are [num_slots, dim/2] or [layers, num_slots, dim/2]")
-        lead, half = tuple(codes.shape[:-1]), codes.shape[-1]
+        lead, half, at = tuple(codes.shape[:-1]), codes.shape[-1], codes.get_device()
         if half % 64 != 0 or half == 0:
             raise ValueError(f"codes: {half} bytes a row are not whole 128-wide heads")
-        _want(codes, "codes", torch.uint8, lead + (half,))
-        _want(scales, "scales", torch.float16, lead + (half // 64,), codes.device)
-        _want(zeros, "zeros", torch.float16, lead + (half // 64,), codes.device)
+        _want(codes, "codes", torch.uint8, lead + (half,), at)
+        _want(scales, "scales", torch.float16, lead + (half // 64,), at)
+        _want(zeros, "zeros", torch.float16, lead + (half // 64,), at)
         self.codes, self.scales, self.zeros = codes, scales, zeros
         self.layered = len(lead) == 2
         self.layers = lead[0] if self.layered else 1
-        self.num_slots, self.dim, self.device = lead[-1], 2 * half, codes.device
+        self.num_slots, self.dim, self.index = lead[-1], 2 * half, at
 
     def layer(self, i: int) -> "KVCacheInt4":
         """Layer i as a cache of its own (views of the same memory)."""
@@ -387,46 +401,41 @@ def kq_attn_decode_int4_kv(q, k_cache: KVCacheInt4, v_cache: KVCacheInt4, k_sign
     `sinks` ones visible.  workspace: empty_attn_workspace(...)."""
     torch = _torch()
     batch, q_heads, _ = q.shape
-    dev, dim = q.device, k_cache.dim
+    at, dim, width = q.get_device(), k_cache.dim, block_table.shape[1]
     if k_cache.layered or v_cache.layered:
         raise ValueError("the attention reads one layer: pass cache.layer(i)")
-    if (v_cache.dim, v_cache.num_slots) != (dim, k_cache.num_slots):
+    if v_cache.dim != dim or v_cache.num_slots != k_cache.num_slots:
         raise ValueError("the key and value caches differ in shape")
-    if k_cache.device != dev or v_cache.device != dev:
-        raise ValueError(f"the caches are not on {dev}")
+    if k_cache.index != at or v_cache.index != at:
+        raise ValueError(f"the caches are not on cuda:{at}")
     shape = (batch, q_heads, 128)
-    _launch(lib().kq_attn_decode_int4_kv, "kq_attn_decode_int4_kv", dev, stream,
-            _want(q, "q", torch.bfloat16, shape), batch, q_heads, dim // 128,
-            None if k_signs is None else _want(k_signs, "k_signs", torch.int8, (dim,), dev),
-            None if v_signs is None else _want(v_signs, "v_signs", torch.int8, (dim,), dev),
+    _launch((_lib or lib()).kq_attn_decode_int4_kv, "kq_attn_decode_int4_kv", at, stream,
+            _want(q, "q", torch.bfloat16, shape, at), batch, q_heads, dim // 128,
+            None if k_signs is None else _want(k_signs, "k_signs", torch.int8, (dim,), at),
+            None if v_signs is None else _want(v_signs, "v_signs", torch.int8, (dim,), at),
             k_cache.codes.data_ptr(), k_cache.scales.data_ptr(), k_cache.zeros.data_ptr(),
             v_cache.codes.data_ptr(), v_cache.scales.data_ptr(), v_cache.zeros.data_ptr(),
-            k_cache.num_slots,
-            _want(block_table, "block_table", torch.int32, (batch, block_table.shape[1]), dev),
-            block_table.shape[1], page_size,
-            _want(seq_lens, "seq_lens", torch.int32, (batch,), dev), window, sinks,
-            softmax_scale, _want(out, "out", torch.bfloat16, shape, dev),
-            _want(workspace, "workspace", torch.uint8, tuple(workspace.shape), dev),
-            workspace.numel())
+            k_cache.num_slots, _want(block_table, "block_table", torch.int32, (batch, width), at),
+            width, page_size, _want(seq_lens, "seq_lens", torch.int32, (batch,), at), window,
+            sinks, softmax_scale, _want(out, "out", torch.bfloat16, shape, at),
+            _want(workspace, "workspace", torch.uint8, workspace.shape, at), workspace.numel())
 
 
 def kq_kv_copy_pages(pairs, page_size: int, k_cache: KVCacheInt4,
                      v_cache: Optional[KVCacheInt4] = None, stream=None) -> None:
     """Copies pages of the cache(s): pairs int32 [n, 2] of (source, destination)
     page; pairs with a page outside the cache are skipped."""
-    torch = _torch()
-    dev = k_cache.device
+    at, n = k_cache.index, pairs.shape[0]
     values = (None, None, None)
     if v_cache is not None:
-        if (v_cache.dim, v_cache.num_slots, v_cache.layers) != \
-                (k_cache.dim, k_cache.num_slots, k_cache.layers):
+        if v_cache.dim != k_cache.dim or v_cache.num_slots != k_cache.num_slots or \
+                v_cache.layers != k_cache.layers:
             raise ValueError("the key and value caches differ in shape")
-        if v_cache.device != dev:
-            raise ValueError(f"the caches are not both on {dev}")
+        if v_cache.index != at:
+            raise ValueError(f"the caches are not both on cuda:{at}")
         values = (v_cache.codes.data_ptr(), v_cache.scales.data_ptr(), v_cache.zeros.data_ptr())
-    n = pairs.shape[0]
-    _launch(lib().kq_kv_copy_pages, "kq_kv_copy_pages", dev, stream,
-            _want(pairs, "pairs", torch.int32, (n, 2), dev), n, page_size, k_cache.num_slots,
+    _launch((_lib or lib()).kq_kv_copy_pages, "kq_kv_copy_pages", at, stream,
+            _want(pairs, "pairs", _torch().int32, (n, 2), at), n, page_size, k_cache.num_slots,
             k_cache.layers, k_cache.dim, k_cache.codes.data_ptr(), k_cache.scales.data_ptr(),
             k_cache.zeros.data_ptr(), *values)
 
