@@ -69,7 +69,8 @@ struct Params {
   int x_bf16, y_bf16;
   int tiles;                              // 16-row tiles of a cluster
   int seg;                                // groups whose x is staged at a time
-  int parts;                              // warps that share a tile's groups in a CTA
+  int parts, part_shift, part;            // warps that share a tile's groups: 2^part_shift, steps
+                                          // of each
   int ranks, rank_shift;                  // CTAs of a cluster, which split k: 2^rank_shift
   int wide;                               // scales of a step's row by aligned copies
   uint32_t recip;                         // 2^16 / m, rounded up
@@ -142,25 +143,33 @@ __device__ __forceinline__ Eight load8(const Params& P, int tok, int k0) {
 // carry a factor 16, or in their own order for the converted E2M1 codes.  Columns
 // behind the last one are left as they are: what they hold reaches no other
 // column, and their sums are not stored.
+template <int NT>
+__device__ __forceinline__ Eight load_x(const Params& P, int g0, int ng, int round) {
+  const int i = (threadIdx.x >> 4) + round * (Shape<NT>::kThreads / 16);
+  const int gi = (int)(i * P.recip >> 16), tok = i - gi * P.m;
+  return load8(P, i < ng * P.m ? tok : P.m, (g0 + gi) * 128 + 8 * (threadIdx.x & 15));
+}
+// `first`: what load_x gave for round 0, loaded before the codes' copies.
 template <bool INT4, int NT>
-__device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, uint4* xs, float2* xf) {
-  constexpr int kAhead = NT == 1 ? 2 : 4;
+__device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, const Eight& first,
+                                        uint4* xs, float2* xf) {
+  constexpr int kAhead = 4, kThreads = Shape<NT>::kThreads;
   const int lane16 = threadIdx.x & 15, slot = threadIdx.x >> 4;
   const int items = ng * P.m;
-  constexpr int kThreads = Shape<NT>::kThreads;
-  for (int i0 = slot; i0 < items + slot; i0 += kAhead * (kThreads / 16)) {
+  const int rounds = (items + kThreads / 16 - 1) / (kThreads / 16);
+#pragma unroll 1
+  for (int r0 = 0; r0 < rounds; r0 += kAhead) {
     Eight in[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int i = i0 + u * (kThreads / 16);
-      const int gi = (int)(i * P.recip >> 16), tok = i - gi * P.m;
-      in[u] = load8(P, i < items ? tok : P.m, (g0 + gi) * 128 + 8 * lane16);
+      in[u] = first;
+      if (r0 + u > 0 && r0 + u < rounds) in[u] = load_x<NT>(P, g0, ng, r0 + u);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int i = i0 + u * (kThreads / 16);
+      if (r0 + u >= rounds) break;
+      const int i = slot + (r0 + u) * (kThreads / 16);
       const int gi = (int)(i * P.recip >> 16), tok = i - gi * P.m;
-      if (__all_sync(0xffffffffu, i >= items)) break;
       float v[8];
       if (P.x_bf16) {
         const uint32_t w[4] = {in[u].a.x, in[u].a.y, in[u].a.z, in[u].a.w};
@@ -440,52 +449,64 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   const int gbegin = rank_begin(P, rank), gend = rank_begin(P, rank + 1);
   for (int g0 = gbegin; g0 < gend; g0 += P.seg) {
     const int ng = min(P.seg, gend - g0), steps = (ng + kStep - 1) / kStep;
-    const int units = tiles * parts;
-    // the steps of a part: an even share of the segment's
-    auto from = [&](int part) { return (int)((uint32_t)(part * steps) / (uint32_t)parts); };
-    int funit = warp, fstep = 0, fend = 0, fill = 0;      // copied next
+    // a warp's units: every kWarps-th (tile, part); a part is P.part steps
+    struct Unit {
+      int tile, part;
+    };
+    const Unit begin{warp >> P.part_shift, warp & (parts - 1)};
+    auto next = [&](Unit& u) {
+      u.tile += kWarps >> P.part_shift;
+      u.part += kWarps & (parts - 1);
+      if (u.part >= parts) {
+        u.part -= parts;
+        ++u.tile;
+      }
+    };
+    Unit fu = begin;                      // copied next
+    int fstep = 0, fend = 0, fill = 0;
     Stream<FMT> stream;
     auto open = [&] {
-      while (funit < units) {
-        const int tile = funit / parts, part = funit - tile * parts;
-        fstep = from(part);
-        fend = from(part + 1);
-        stream.start(P, row0 + 16 * tile);
-        if (fstep < fend) return;
-        funit += kWarps;
+      for (; fu.tile < tiles; next(fu)) {
+        fstep = fu.part * P.part;
+        fend = min(fstep + P.part, steps);
+        if (fstep < fend) {
+          stream.start(P, row0 + 16 * fu.tile);
+          return;
+        }
       }
     };
     auto fetch = [&] {
-      if (funit < units) {
+      if (fu.tile < tiles) {
         stream.copy(P, g0 + fstep * kStep, g0 + ng, ring + fill * kStage);
         if (++fill == S::kStages) fill = 0;
         if (++fstep == fend) {
-          funit += kWarps;
+          next(fu);
           open();
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    const Eight x0 = load_x<NT>(P, g0, ng, 0);
     open();
 #pragma unroll 1
     for (int i = 0; i < S::kStages; ++i) fetch();
     if (g0 > gbegin) __syncthreads();     // the last segment's x is no longer read
-    stage_x<INT4, NT>(P, g0, ng, xs, xf);
+    stage_x<INT4, NT>(P, g0, ng, x0, xs, xf);
     __syncthreads();
     if (!started) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     started = true;
     int stage = 0;
 #pragma unroll 1
-    for (int unit = warp; unit < units; unit += kWarps) {
-      const int tile = unit / parts, part = unit - tile * parts;
-      const int s1 = from(part + 1);
+    for (Unit u = begin; u.tile < tiles; next(u)) {
+      const int tile = u.tile, part = u.part;
+      const int s0 = part * P.part, s1 = min(s0 + P.part, steps);
       float acc[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
 #pragma unroll 1
-      for (int step = from(part); step < s1; ++step) {
+      for (int step = s0; step < s1; ++step) {
         asm volatile("cp.async.wait_group %0;" :: "n"(S::kStages - 1) : "memory");
         __syncwarp();
         compute_step<FMT, NT>(ring + stage * kStage, step * kStep, ng - step * kStep, xs, xf, acc);
@@ -622,14 +643,15 @@ cudaError_t launch(Params P, cudaStream_t s) {
   P.tiles = (int)(tiles < 1 ? 1 : tiles);
   // parts: the shortest way through the units for the CTA's warps
   const int steps = P.seg / kStep, own = (P.tiles + ranks - 1) / ranks;
-  P.parts = 1;
   int best = 1 << 30;
-  for (int p = 1; p <= steps && p * own * ranks <= room; ++p) {
+  for (int shift = 0, p = 1; (shift == 0 || p <= steps) && p * own * ranks <= room; ++shift, p *= 2) {
     const int rounds = (P.tiles * p + Shape<NT>::kWarps - 1) / Shape<NT>::kWarps;
-    const int way = rounds * ((steps + p - 1) / p);
+    const int part = (steps + p - 1) / p, way = rounds * part;
     if (way < best) {
       best = way;
       P.parts = p;
+      P.part_shift = shift;
+      P.part = part;
     }
   }
   const size_t smem = R::kRings + (size_t)P.seg * NT * (2048 + 64) +
@@ -663,7 +685,7 @@ cudaError_t launch_gemv(int fmt, const void* x, int x_bf16, int m, const uint8_t
                         const void* scales, const void* zeros, const float* tscale, int64_t n,
                         int k, void* y, int y_bf16, cudaStream_t s) {
   const gv::Params P{x, codes, scales, static_cast<const uint16_t*>(zeros), tscale, y, n, m, k,
-                     (k + 127) / 128, x_bf16, y_bf16, 0, 0, 0, 1, 0, 0, 0};
+                     (k + 127) / 128, x_bf16, y_bf16, 0, 0, 1, 0, 0, 1, 0, 0, 0};
   switch (fmt) {
     case KQ_FMT_INT4_SYM: return gv::launch_tiles<KQ_FMT_INT4_SYM>(P, s);
     case KQ_FMT_INT4_ASYM: return gv::launch_tiles<KQ_FMT_INT4_ASYM>(P, s);
