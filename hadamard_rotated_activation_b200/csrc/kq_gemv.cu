@@ -16,7 +16,9 @@
 //   MXFP4  likewise, the block's power of two taken relative to the largest of
 //          the row's four blocks in the group (exact down to 2^-23 of it).
 // x is held per token and group of 128 as fp16 with a power of two that puts its
-// largest element in [2^14, 2^15): bf16 rows are exact down to 2^-28 of it.
+// largest element in [2^14, 2^15), or in [1, 2) beside E2M1 codes (whose block sums
+// must not overflow): bf16 rows are exact down to 2^-31 or 2^-17 of it, and off by
+// at most 2^-25 of it below.
 // fp32 rows are two columns, the rounded value and 2^11 times what it leaves.
 // A group's sum leaves the tensor core after 8 steps and is added in fp32.
 //
@@ -45,7 +47,8 @@ using sm100::pow2f;
 // A warp streams its rows in steps of 16 rows by kStep groups, kStages of which are
 // on their way or in use.  Up to two tiles of 8 columns: two CTAs of 8 warps an
 // SM.  Four tiles: one CTA of 16 warps, which stages x once an SM.
-constexpr int kStep = 2;
+constexpr int kStep = 4;
+constexpr int kStages = 2;
 constexpr int kRow = kStep * 64;                  // bytes of a staged row of codes
 constexpr int kScaleRow = kStep * 8;              // bytes of its scales at most
 constexpr int kStage = 16 * (kRow + kScaleRow);
@@ -54,7 +57,6 @@ struct Shape {
   static constexpr int kWarps = NT == 4 ? 16 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = NT == 4 ? 1 : 2;
-  static constexpr int kStages = NT == 4 ? 3 : 4;
 };
 
 struct Params {
@@ -150,7 +152,7 @@ __device__ __forceinline__ Eight load_x(const Params& P, int g0, int ng, int rou
   return load8(P, i < ng * P.m ? tok : P.m, (g0 + gi) * 128 + 8 * (threadIdx.x & 15));
 }
 // `first`: what load_x gave for round 0, loaded before the codes' copies.
-template <bool INT4, int NT>
+template <bool INT4, bool BLOCKS, int NT>
 __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, const Eight& first,
                                         uint4* xs, float2* xf) {
   constexpr int kAhead = 4, kThreads = Shape<NT>::kThreads;
@@ -189,7 +191,8 @@ __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, const E
       for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int sh = top > 0.0f ? min(141 - (int)(__float_as_uint(top) >> 23), 126) : 0;
+      const int sh =
+          top > 0.0f ? min((INT4 ? 141 : 127) - (int)(__float_as_uint(top) >> 23), 126) : 0;
       const float up = pow2f(sh);
       float sum = 0.0f;
 #pragma unroll
@@ -202,7 +205,8 @@ __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, const E
         for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       }
       if (i < items) {
-        const int t = lane16 >> 2, j = lane16 & 3;
+        // block by block, a lane's 8 elements of block j begin at 32 j + 8 t
+        const int t = BLOCKS ? lane16 & 3 : lane16 >> 2, j = BLOCKS ? lane16 >> 2 : lane16 & 3;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           if (part == 1 && P.x_bf16) break;
@@ -237,30 +241,43 @@ __device__ __forceinline__ int rank_begin(const Params& P, int rank) {
   return (int)((uint32_t)(rank * P.groups) >> P.rank_shift);
 }
 
+// Whether a format's blocks are summed one by one (MXFP4 with few columns): a
+// block's two mma steps leave the tensor core and are scaled in fp32, which costs
+// 16 multiply-adds a group and tile of 8 columns instead of 32 products of codes
+// and scales.
+template <int FMT, int NT>
+constexpr bool kByBlock = FMT == KQ_FMT_MXFP4 && NT == 1;
+
+// Where the 16-byte piece c of row r is staged.  Fragment reads take four pieces of
+// two neighbouring rows at a time, or, block by block, 4 bytes of one piece of eight
+// rows; either order has no bank conflicts.
+template <bool BLOCKS>
+__device__ __forceinline__ int piece(int r, int c) {
+  return 16 * (c ^ (BLOCKS ? r & 7 : (r & 1) << 2));
+}
+
 // A warp's stream through the codes: the rows it is at, and the lane's share of
-// the copies of a step.  8 lanes a row, 4 rows at a time; the 16-byte piece c of row
-// r is staged at c ^ 4 (r & 1), which keeps the fragment reads (two rows by four
-// pieces at a time) free of bank conflicts.
-template <int FMT>
+// the copies of a step (16 lanes a row, 2 rows at a time).
+template <int FMT, bool BLOCKS>
 struct Stream {
   const uint8_t* codes;                   // row0, the lane's piece
   const uint8_t* scales;                  // the lane's row of scales (zero points)
-  int off[4];                             // bytes to the lane's rows (the last row again behind it)
+  int off[8];                             // bytes to the lane's rows (the last row again behind it)
   int64_t row0;
 
   __device__ __forceinline__ void start(const Params& P, int64_t row) {
     const int lane = threadIdx.x & 31;
     const int left = (int)min(P.n - 1 - row, (int64_t)15);
     row0 = row;
-    codes = P.codes + row * (P.k / 2) + 16 * (lane & 7);
+    codes = P.codes + row * (P.k / 2) + 16 * (lane & 15);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) off[i] = min(left, 4 * i + (lane >> 3)) * (P.k / 2);
+    for (int i = 0; i < 8; ++i) off[i] = min(left, 2 * i + (lane >> 4)) * (P.k / 2);
     const int64_t sr = row + min(left, lane & 15);
     if (FMT == KQ_FMT_INT4_ASYM)
       scales = reinterpret_cast<const uint8_t*>(
           (lane < 16 ? static_cast<const uint16_t*>(P.scales) : P.zeros) + sr * P.groups);
     else if (FMT == KQ_FMT_NVFP4)
-      scales = static_cast<const uint8_t*>(P.scales) + sr * (P.k / 16);
+      scales = static_cast<const uint8_t*>(P.scales) + sr * (P.k / 16) + 16 * (lane >> 4);
     else if (FMT == KQ_FMT_MXFP4)
       scales = static_cast<const uint8_t*>(P.scales) + sr * (P.k / 32);
   }
@@ -269,20 +286,22 @@ struct Stream {
   // behind them 16 rows of scales: INT4 asymmetric kStep fp16 scales and zero
   // points, NVFP4 8 E4M3 bytes a group, MXFP4 4 E8M0 bytes a group.
   __device__ __forceinline__ void copy(const Params& P, int g0, int gend, uint8_t* stage) const {
-    const int lane = threadIdx.x & 31, c = lane & 7, r = lane >> 3;
+    const int lane = threadIdx.x & 31, c = lane & 15, r = lane >> 4;
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(stage);
     const bool in = g0 + (c >> 2) < gend && g0 * 128 + 32 * c < P.k;
     const uint8_t* from = codes + (in ? g0 * 64 : 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      copy_async<16>(to + (4 * i + r) * kRow + 16 * (c ^ ((r & 1) << 2)), from + off[i], in);
+    for (int i = 0; i < 8; ++i)
+      copy_async<16>(to + (2 * i + r) * kRow + piece<BLOCKS>(2 * i + r, c), from + off[i], in);
     if (FMT == KQ_FMT_INT4_SYM) return;
     const uint32_t ts = to + 16 * kRow + (lane & 15) * kScaleRow;
     if (P.wide) {
       if (FMT == KQ_FMT_INT4_ASYM)
-        copy_async<4>(ts + (lane >> 4) * 4, scales + 2 * g0);
+        copy_async<8>(ts + (lane >> 4) * 8, scales + 2 * g0);
+      else if (FMT == KQ_FMT_NVFP4)
+        copy_async<16>(ts + (lane >> 4) * 16, scales + 8 * g0);
       else if (lane < 16)
-        copy_async<FMT == KQ_FMT_NVFP4 ? 16 : 8>(ts, scales + (FMT == KQ_FMT_NVFP4 ? 8 : 4) * g0);
+        copy_async<16>(ts, scales + 4 * g0);
       return;
     }
     // scales that no aligned copy reaches: one by one
@@ -311,7 +330,8 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
                                              const float2* xf, float (&acc)[NT][4]) {
   constexpr bool INT4 = FMT == KQ_FMT_INT4_SYM || FMT == KQ_FMT_INT4_ASYM;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint8_t* ca = stage + g * kRow + 16 * t;
+  constexpr bool BLOCKS = kByBlock<FMT, NT>;
+  const uint8_t* ca = stage + g * kRow;
   const uint8_t* sca = stage + 16 * kRow + g * kScaleRow;
   constexpr int kDown = 8 * kScaleRow;            // from row g to row g + 8
   const uint4* xg = xs + gl * NT * 128 + lane;
@@ -319,7 +339,37 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
 #pragma unroll
   for (int i = 0; i < kStep; ++i, xg += NT * 128, fg += NT * 8) {
     if (i >= ng) break;
-    const int at = 64 * (i ^ (g & 1));
+    if constexpr (BLOCKS) {
+      // block b: 8 codes a lane; 2^e c_b of the four blocks, then the token's scale
+      const uint32_t ea = *reinterpret_cast<const uint32_t*>(sca + 4 * i);
+      const uint32_t eb = *reinterpret_cast<const uint32_t*>(sca + kDown + 4 * i);
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int at = piece<true>(g, 4 * i + b) + 4 * t;
+        uint32_t fa[4], fb[4];
+        e2m1_halves(*reinterpret_cast<const uint32_t*>(ca + at), fa);
+        e2m1_halves(*reinterpret_cast<const uint32_t*>(ca + 8 * kRow + at), fb);
+        const uint4 x = xg[b * 32];
+        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        mma16816(c, fa[0], fb[0], fa[1], fb[1], x.x, x.y);
+        mma16816(c, fa[2], fb[2], fa[3], fb[3], x.z, x.w);
+        // 2^(e - 127); the smallest, e = 0, is subnormal
+        const float pa = __uint_as_float(max(ea >> (8 * b) << 24 >> 1, 0x00400000u));
+        const float pb = __uint_as_float(max(eb >> (8 * b) << 24 >> 1, 0x00400000u));
+        sum[0] = fmaf(pa, c[0], sum[0]);
+        sum[1] = fmaf(pa, c[1], sum[1]);
+        sum[2] = fmaf(pb, c[2], sum[2]);
+        sum[3] = fmaf(pb, c[3], sum[3]);
+      }
+      const float4 f = *reinterpret_cast<const float4*>(fg);
+      acc[0][0] = fmaf(f.x, sum[0], acc[0][0]);
+      acc[0][1] = fmaf(f.z, sum[1], acc[0][1]);
+      acc[0][2] = fmaf(f.x, sum[2], acc[0][2]);
+      acc[0][3] = fmaf(f.z, sum[3], acc[0][3]);
+      continue;
+    }
+    const int at = piece<false>(g, 4 * i + t);
     const uint4 wa = *reinterpret_cast<const uint4*>(ca + at);
     const uint4 wb = *reinterpret_cast<const uint4*>(ca + 8 * kRow + at);
     const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
@@ -431,12 +481,13 @@ template <int FMT, int NT>
 __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(Params P) {
   using S = Shape<NT>;
   constexpr bool INT4 = FMT == KQ_FMT_INT4_SYM || FMT == KQ_FMT_INT4_ASYM;
+  constexpr bool BLOCKS = kByBlock<FMT, NT>;
   constexpr int kWarps = S::kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   const int ranks = P.ranks, rank = ranks > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * (S::kStages * kStage);
-  uint4* xs = reinterpret_cast<uint4*>(smem + kWarps * S::kStages * kStage);
+  uint8_t* ring = smem + warp * (kStages * kStage);
+  uint4* xs = reinterpret_cast<uint4*>(smem + kWarps * kStages * kStage);
   float2* xf = reinterpret_cast<float2*>(xs + P.seg * NT * 128);
   float* red = reinterpret_cast<float*>(xf + P.seg * NT * 8);
   // the others' shared memory may be written once they have all started
@@ -464,7 +515,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
     };
     Unit fu = begin;                      // copied next
     int fstep = 0, fend = 0, fill = 0;
-    Stream<FMT> stream;
+    Stream<FMT, BLOCKS> stream;
     auto open = [&] {
       for (; fu.tile < tiles; next(fu)) {
         fstep = fu.part * P.part;
@@ -478,7 +529,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
     auto fetch = [&] {
       if (fu.tile < tiles) {
         stream.copy(P, g0 + fstep * kStep, g0 + ng, ring + fill * kStage);
-        if (++fill == S::kStages) fill = 0;
+        if (++fill == kStages) fill = 0;
         if (++fstep == fend) {
           next(fu);
           open();
@@ -489,9 +540,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
     const Eight x0 = load_x<NT>(P, g0, ng, 0);
     open();
 #pragma unroll 1
-    for (int i = 0; i < S::kStages; ++i) fetch();
+    for (int i = 0; i < kStages; ++i) fetch();
     if (g0 > gbegin) __syncthreads();     // the last segment's x is no longer read
-    stage_x<INT4, NT>(P, g0, ng, x0, xs, xf);
+    stage_x<INT4, BLOCKS, NT>(P, g0, ng, x0, xs, xf);
     __syncthreads();
     if (!started) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     started = true;
@@ -507,11 +558,11 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
         for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
 #pragma unroll 1
       for (int step = s0; step < s1; ++step) {
-        asm volatile("cp.async.wait_group %0;" :: "n"(S::kStages - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
         __syncwarp();
         compute_step<FMT, NT>(ring + stage * kStage, step * kStep, ng - step * kStep, xs, xf, acc);
         __syncwarp();                     // the stage is free
-        if (++stage == S::kStages) stage = 0;
+        if (++stage == kStages) stage = 0;
         fetch();
       }
       const int owner = tile & (ranks - 1);
@@ -544,21 +595,23 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   } else {
     __syncthreads();
   }
-  // ---- join: the ranks' batches in order; consecutive threads take consecutive
-  // rows of one token
-  const int mine = ((tiles - rank + ranks - 1) >> P.rank_shift) * 16;   // rows this CTA owns
-  for (int i = threadIdx.x; i < mine * mt; i += Shape<NT>::kThreads) {
-    const int tok = i / mine, r = i - tok * mine;
-    const int64_t row = row0 + (int64_t)((r >> 4) * ranks + rank) * 16 + (r & 15);
-    if (row >= P.n) continue;
-    const float* from = red + (size_t)r * mt + tok;
+  // ---- join: the ranks' and parts' sums in order; a warp takes a tile by two tokens,
+  // a lane a row
+  const int mine = (tiles - rank + ranks - 1) >> P.rank_shift;    // tiles this CTA owns
+  const int pairs = (mt + 1) >> 1, slots = ranks * parts, pitch = own * 16 * mt;
+  const float t_scale = FMT == KQ_FMT_NVFP4 ? __ldg(P.tscale) : 1.0f;
+  for (int q = warp; q < mine * pairs; q += kWarps) {
+    const int tl = q / pairs, tok = 2 * (q - tl * pairs) + (lane >> 4), r = lane & 15;
+    const int64_t row = row0 + ((tl << P.rank_shift) + rank) * 16 + r;
+    if (tok >= mt || row >= P.n) continue;
+    const float* from = red + (tl * 16 + r) * mt + tok;
     float v = 0.0f;
-#pragma unroll 4
-    for (int c = 0; c < ranks * parts; ++c) v += from[(size_t)c * own * 16 * mt];
+#pragma unroll 8
+    for (int c = 0; c < slots; ++c) v += from[c * pitch];
     if (INT4) v *= 0x1p24f;               // the codes' 2^-24
-    if (FMT == KQ_FMT_INT4_SYM) v *= static_cast<const float*>(P.scales)[row];
-    if (FMT == KQ_FMT_NVFP4) v *= *P.tscale;
-    const int64_t at = (int64_t)tok * P.n + row;
+    if (FMT == KQ_FMT_INT4_SYM) v *= __ldg(static_cast<const float*>(P.scales) + row);
+    if (FMT == KQ_FMT_NVFP4) v *= t_scale;
+    const int64_t at = tok * P.n + row;
     if (P.y_bf16)
       static_cast<__nv_bfloat16*>(P.y)[at] = __float2bfloat16_rn(v);
     else
@@ -566,14 +619,16 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   }
 }
 
-#ifndef KQ_RANKS
-#define KQ_RANKS 4
-#endif
+// CTAs that split k.  8 took the 4096 x 4096 product of one token from 6.3 to 6.6 us
+// (the cluster barrier), 2 the 12288 x 4096 one of eight from 14.6 to 16.2 (each CTA
+// stages more of x).
+constexpr int kSplit = 4;
+
 // Shared memory of a CTA: the stages, x of a segment, the sums.
 template <int NT>
 struct Room {
   static constexpr int kAll = (Shape<NT>::kCtas == 1 ? 227 : 113) * 1024;
-  static constexpr int kRings = Shape<NT>::kWarps * Shape<NT>::kStages * kStage;
+  static constexpr int kRings = Shape<NT>::kWarps * kStages * kStage;
   static constexpr int kSums = 12 * 1024;
   static constexpr int kGroups = (kAll - kRings - kSums) / (NT * (2048 + 64)) / kStep * kStep;
   static_assert(kGroups >= 4, "room for x");
@@ -618,7 +673,7 @@ template <int FMT, int NT>
 cudaError_t launch(Params P, cudaStream_t s) {
   using R = Room<NT>;
   int ranks = 1;
-  while (ranks < KQ_RANKS && P.groups / (2 * ranks) >= kStep) ranks *= 2;
+  while (ranks < kSplit && P.groups / (2 * ranks) >= kStep) ranks *= 2;
   while (ranks < 8 && P.groups > ranks * R::kGroups) ranks *= 2;
   P.ranks = ranks;
   for (P.rank_shift = 0; 1 << P.rank_shift < ranks;) ++P.rank_shift;
@@ -635,7 +690,7 @@ cudaError_t launch(Params P, cudaStream_t s) {
   // row begins at a multiple of kStep groups
   const uintptr_t at = reinterpret_cast<uintptr_t>(P.scales) | reinterpret_cast<uintptr_t>(P.zeros);
   P.wide = P.groups % (kStep * ranks) == 0 && P.k % 128 == 0 &&
-           at % (FMT == KQ_FMT_INT4_ASYM ? 4 : FMT == KQ_FMT_NVFP4 ? 16 : 8) == 0;
+           at % (FMT == KQ_FMT_INT4_ASYM ? 8 : 16) == 0;
   // rows for one round of CTAs, as far as their sums fit
   int64_t tiles = (all + ctas / ranks - 1) / (ctas / ranks);
   const int64_t room = R::kSums / (P.m * 64);           // tiles times parts, and a rank's rounding
