@@ -336,9 +336,7 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
   constexpr int kDown = 8 * kScaleRow;            // from row g to row g + 8
   const uint4* xg = xs + gl * NT * 128 + lane;
   const float2* fg = xf + gl * NT * 8 + 2 * t;
-#pragma unroll
-  for (int i = 0; i < kStep; ++i, xg += NT * 128, fg += NT * 8) {
-    if (i >= ng) break;
+  auto group = [&](int i) {
     if constexpr (BLOCKS) {
       // block b: 8 codes a lane; 2^e c_b of the four blocks, then the token's scale
       const uint32_t ea = *reinterpret_cast<const uint32_t*>(sca + 4 * i);
@@ -367,7 +365,7 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
       acc[0][1] = fmaf(f.z, sum[1], acc[0][1]);
       acc[0][2] = fmaf(f.x, sum[2], acc[0][2]);
       acc[0][3] = fmaf(f.z, sum[3], acc[0][3]);
-      continue;
+      return;
     }
     const int at = piece<false>(g, 4 * i + t);
     const uint4 wa = *reinterpret_cast<const uint4*>(ca + at);
@@ -465,6 +463,19 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
         acc[n][2] = fmaf(c[n][2] * f.x, sb, acc[n][2]);
         acc[n][3] = fmaf(c[n][3] * f.z, sb, acc[n][3]);
       }
+    }
+  };
+  if (NT == 1 && ng >= kStep) {           // whole steps without a branch between groups
+#pragma unroll
+    for (int i = 0; i < kStep; ++i, xg += NT * 128, fg += NT * 8) group(i);
+  } else if (NT == 1) {
+#pragma unroll 1
+    for (int i = 0; i < ng; ++i, xg += NT * 128, fg += NT * 8) group(i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kStep; ++i, xg += NT * 128, fg += NT * 8) {
+      if (i >= ng) break;
+      group(i);
     }
   }
 }
