@@ -54,7 +54,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSlack = 6;
 constexpr int kCols = 8;                      // query heads a unit carries
 constexpr int kMaxCtas = 320;
-constexpr int kMinTiles = 2;                  // tiles a CTA takes at least
+constexpr int kMinTiles = 1;                  // tiles a CTA takes at least
 // What beginning a unit costs, in tiles: the query's rotation and the end of the
 // unit before it.  The tiles are dealt with so many more in front of each unit.
 constexpr int kUnitCost = 2;
