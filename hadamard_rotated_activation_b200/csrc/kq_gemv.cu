@@ -7,10 +7,15 @@
 // Mathematics.  The contraction runs on the bare codes, with the tokens as
 // columns of mma.sync (m16n8k16, fp16 operands, fp32 sums) and 16 weight rows
 // as its rows:
-//   INT4   a code masked out of its word is an fp16 number (u 2^-24, or
-//          16 u 2^-24 for the upper nibble of a byte), so a word of 8 codes
+//   INT4, bf16 result: a code masked out of its word is an fp16 number (u 2^-24,
+//          or 16 u 2^-24 for the upper nibble of a byte), so a word of 8 codes
 //          costs 5 integer operations; the 16 is taken out of x.  Per group of
-//          128: s (2^24 sum u x - z sum x); symmetric codes are u - 8.
+//          128: s (2^24 sum u x - z sum x); symmetric codes are u - 8.  The tensor
+//          core lines up such subnormal operands as if they were 2^-14, which
+//          costs 6 to 10 of its 25 bits: results are off by 5e-6, far inside bf16.
+//   INT4, fp32 result: the masked code under the exponent of 1024, then 4 fp16
+//          operations a word that take 1024 and the offset 8 away again: u - 8,
+//          exactly, in full alignment (off by 2e-7); z - 8 takes the place of z.
 //   NVFP4  E2M1 codes by the hardware conversion, times the block's E4M3 scale:
 //          at most 6 significant bits, exact in fp16.
 //   MXFP4  likewise, the block's power of two taken relative to the largest of
@@ -100,6 +105,16 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t add_h2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 __device__ __forceinline__ float half_value(uint32_t h) {
   return __half2float(__ushort_as_half((unsigned short)h));
 }
@@ -122,6 +137,19 @@ __device__ __forceinline__ float2 half2_floats(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Eight INT4 codes (offset codes: symmetric ones with their sign bit turned) -> u - 8
+// as fp16 pairs (0,4) (1,5) (2,6) (3,7).
+template <bool TURN>
+__device__ __forceinline__ void code_halves(uint32_t w, uint32_t (&h)[4]) {
+  // 1024 + u and 1024 + 16 u, then - 1032 and / 16 - 72: every step is exact
+  constexpr uint32_t lo = TURN ? 0x64086408u : 0x64006400u, hi = TURN ? 0x64806480u : 0x64006400u;
+  const uint32_t v = w >> 8;
+  h[0] = add_h2((w & 0x000f000fu) ^ lo, 0xe408e408u);
+  h[1] = fma_h2((w & 0x00f000f0u) ^ hi, 0x2c002c00u, 0xd480d480u);
+  h[2] = add_h2((v & 0x000f000fu) ^ lo, 0xe408e408u);
+  h[3] = fma_h2((v & 0x00f000f0u) ^ hi, 0x2c002c00u, 0xd480d480u);
+}
+
 // Eight elements of a row of x as loaded.
 struct Eight {
   uint4 a, b;
@@ -141,8 +169,9 @@ __device__ __forceinline__ Eight load8(const Params& P, int tok, int k0) {
 // Stages x of groups [g0, g0 + ng) for the columns of NT mma tiles.  16 lanes take
 // one (group, token), a lane 8 consecutive elements, which are one 16-byte piece
 // in fragment order: (group, tile, word j, column, t) holds elements 32 t + 8 j ...
-// as pairs (0,4) (1,5) (2,6) (3,7) for the masked INT4 codes, whose odd ones
-// carry a factor 16, or in their own order for the converted E2M1 codes.  Columns
+// as pairs (0,4) (1,5) (2,6) (3,7) for the masked INT4 codes (PAIRS), whose odd ones
+// carry a factor 16 when they are taken as they are (SMALL), or in their own order
+// for the converted E2M1 codes.  SUMS: the groups' sums too.  Columns
 // behind the last one are left as they are: what they hold reaches no other
 // column, and their sums are not stored.
 template <int NT>
@@ -152,7 +181,7 @@ __device__ __forceinline__ Eight load_x(const Params& P, int g0, int ng, int rou
   return load8(P, i < ng * P.m ? tok : P.m, (g0 + gi) * 128 + 8 * (threadIdx.x & 15));
 }
 // `first`: what load_x gave for round 0, loaded before the codes' copies.
-template <bool INT4, bool BLOCKS, int NT>
+template <bool SMALL, bool SUMS, bool BLOCKS, bool PAIRS, int NT>
 __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, const Eight& first,
                                         uint4* xs, float2* xf) {
   constexpr int kAhead = 4, kThreads = Shape<NT>::kThreads;
@@ -192,7 +221,7 @@ __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, const E
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int sh =
-          top > 0.0f ? min((INT4 ? 141 : 127) - (int)(__float_as_uint(top) >> 23), 126) : 0;
+          top > 0.0f ? min((PAIRS ? 141 : 127) - (int)(__float_as_uint(top) >> 23), 126) : 0;
       const float up = pow2f(sh);
       float sum = 0.0f;
 #pragma unroll
@@ -200,7 +229,7 @@ __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, const E
         v[e] *= up;
         sum += v[e];
       }
-      if (INT4) {
+      if (SUMS) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       }
@@ -214,21 +243,21 @@ __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, const E
           uint32_t h[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float& lo = v[INT4 ? e : 2 * e];
-            float& hi = v[INT4 ? e + 4 : 2 * e + 1];
+            float& lo = v[PAIRS ? e : 2 * e];
+            float& hi = v[PAIRS ? e + 4 : 2 * e + 1];
             h[e] = half2_bits(lo, hi);
             if (!P.x_bf16 && part == 0) {
               const float2 r = half2_floats(h[e]);
               lo = (lo - r.x) * 2048.0f;
               hi = (hi - r.y) * 2048.0f;
             }
-            if (INT4 && (e & 1)) h[e] = mul_h2(h[e], 0x2c002c00u);    // / 16
+            if (SMALL && (e & 1)) h[e] = mul_h2(h[e], 0x2c002c00u);   // / 16
           }
           xs[((gi * NT + (col >> 3)) * 4 + j) * 32 + (col & 7) * 4 + t] =
               make_uint4(h[0], h[1], h[2], h[3]);
           // the sum of the group (of both parts at once) rides on the first column
           if (lane16 == 0)
-            xf[gi * NT * 8 + col] = part == 0 ? make_float2(pow2f(-sh), sum * 0x1p-24f)
+            xf[gi * NT * 8 + col] = part == 0 ? make_float2(pow2f(-sh), SMALL ? sum * 0x1p-24f : sum)
                                               : make_float2(pow2f(-sh) * 0x1p-11f, 0.0f);
         }
       }
@@ -325,7 +354,7 @@ struct Stream {
 };
 
 // Adds a staged step: its first ng groups, times groups gl ... of the staged x.
-template <int FMT, int NT>
+template <int FMT, int NT, bool SMALL>
 __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int ng, const uint4* xs,
                                              const float2* xf, float (&acc)[NT][4]) {
   constexpr bool INT4 = FMT == KQ_FMT_INT4_SYM || FMT == KQ_FMT_INT4_ASYM;
@@ -384,8 +413,12 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
       za = half_value(s16[kStep]);
       sb = half_value(s16[kDown / 2]);
       zb = half_value(s16[kDown / 2 + kStep]);
+      if (!SMALL) {
+        za -= 8.0f;
+        zb -= 8.0f;
+      }
     } else if (FMT == KQ_FMT_INT4_SYM) {
-      za = zb = 8.0f;
+      za = zb = SMALL ? 8.0f : 0.0f;
     } else if (FMT == KQ_FMT_NVFP4) {
       // both blocks' E4M3 scales as fp16, each in both halves
       const uint32_t ba = *reinterpret_cast<const uint16_t*>(sca + 8 * i + 2 * t);
@@ -416,7 +449,10 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t fa[4], fb[4];
-      if (INT4) {
+      if (INT4 && !SMALL) {
+        code_halves<FMT == KQ_FMT_INT4_SYM>(xa[j], fa);
+        code_halves<FMT == KQ_FMT_INT4_SYM>(xb[j], fb);
+      } else if (INT4) {
         // symmetric codes are offset by 8
         constexpr uint32_t lo = FMT == KQ_FMT_INT4_SYM ? 0x00080008u : 0u, hi = lo << 4;
         fa[0] = (xa[j] & 0x000f000fu) ^ lo;
@@ -488,7 +524,8 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
 // own in the shared memory of the CTA that owns the tile; behind one cluster
 // barrier the owners add them up in order.  (Measured instead: sums read from the
 // others' shared memory behind the barrier cost 0.5 us a CTA of the cluster.)
-template <int FMT, int NT>
+// SMALL: INT4 codes as subnormal operands (bf16 results).
+template <int FMT, int NT, bool SMALL>
 __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(Params P) {
   using S = Shape<NT>;
   constexpr bool INT4 = FMT == KQ_FMT_INT4_SYM || FMT == KQ_FMT_INT4_ASYM;
@@ -553,7 +590,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) fetch();
     if (g0 > gbegin) __syncthreads();     // the last segment's x is no longer read
-    stage_x<INT4, BLOCKS, NT>(P, g0, ng, x0, xs, xf);
+    constexpr bool SUMS = FMT == KQ_FMT_INT4_ASYM || (FMT == KQ_FMT_INT4_SYM && SMALL);
+    stage_x<SMALL, SUMS, BLOCKS, INT4, NT>(P, g0, ng, x0, xs, xf);
     __syncthreads();
     if (!started) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     started = true;
@@ -571,7 +609,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
       for (int step = s0; step < s1; ++step) {
         asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
         __syncwarp();
-        compute_step<FMT, NT>(ring + stage * kStage, step * kStep, ng - step * kStep, xs, xf, acc);
+        compute_step<FMT, NT, SMALL>(ring + stage * kStage, step * kStep, ng - step * kStep, xs, xf, acc);
         __syncwarp();                     // the stage is free
         if (++stage == kStages) stage = 0;
         fetch();
@@ -619,7 +657,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
     float v = 0.0f;
 #pragma unroll 8
     for (int c = 0; c < slots; ++c) v += from[c * pitch];
-    if (INT4) v *= 0x1p24f;               // the codes' 2^-24
+    if (SMALL) v *= 0x1p24f;              // the codes' 2^-24
     if (FMT == KQ_FMT_INT4_SYM) v *= __ldg(static_cast<const float*>(P.scales) + row);
     if (FMT == KQ_FMT_NVFP4) v *= t_scale;
     const int64_t at = tok * P.n + row;
@@ -647,7 +685,7 @@ struct Room {
 
 // CTAs of clusters of `ranks` that the current device holds at a time: a cluster
 // stays within a GPC, so it is less than all SMs hold.  Looked up once.
-template <int FMT, int NT>
+template <int FMT, int NT, bool SMALL>
 cudaError_t resident_ctas(int ranks, int* out) {
   // the attribute set here holds for every launch of this kernel on the device
   constexpr int kDevices = 64;
@@ -659,7 +697,7 @@ cudaError_t resident_ctas(int ranks, int* out) {
   if (dev < kDevices && (*out = known[dev][i].load(std::memory_order_relaxed)) > 0)
     return cudaSuccess;
   const size_t smem = Room<NT>::kAll;
-  e = cudaFuncSetAttribute((const void*)k_gemv<FMT, NT>,
+  e = cudaFuncSetAttribute((const void*)k_gemv<FMT, NT, SMALL>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -673,14 +711,14 @@ cudaError_t resident_ctas(int ranks, int* out) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int clusters = 0;
-  e = cudaOccupancyMaxActiveClusters(&clusters, (const void*)k_gemv<FMT, NT>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&clusters, (const void*)k_gemv<FMT, NT, SMALL>, &cfg);
   if (e != cudaSuccess) return e;
   *out = clusters * ranks;
   if (dev < kDevices) known[dev][i].store(*out, std::memory_order_relaxed);
   return cudaSuccess;
 }
 
-template <int FMT, int NT>
+template <int FMT, int NT, bool SMALL>
 cudaError_t launch(Params P, cudaStream_t s) {
   using R = Room<NT>;
   int ranks = 1;
@@ -689,7 +727,7 @@ cudaError_t launch(Params P, cudaStream_t s) {
   P.ranks = ranks;
   for (P.rank_shift = 0; 1 << P.rank_shift < ranks;) ++P.rank_shift;
   int ctas = 0;
-  cudaError_t e = resident_ctas<FMT, NT>(ranks, &ctas);
+  cudaError_t e = resident_ctas<FMT, NT, SMALL>(ranks, &ctas);
   if (e != cudaSuccess) return e;
   const int64_t all = (P.n + 15) / 16;
   // x of a CTA's groups in one piece where there is room
@@ -734,15 +772,15 @@ cudaError_t launch(Params P, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ranks > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_gemv<FMT, NT>, P);
+  return cudaLaunchKernelEx(&cfg, k_gemv<FMT, NT, SMALL>, P);
 }
 
-template <int FMT>
+template <int FMT, bool SMALL>
 cudaError_t launch_tiles(const Params& P, cudaStream_t s) {
   const int cols = P.x_bf16 ? P.m : 2 * P.m;
-  if (cols <= 8) return launch<FMT, 1>(P, s);
-  if (cols <= 16) return launch<FMT, 2>(P, s);
-  return launch<FMT, 4>(P, s);
+  if (cols <= 8) return launch<FMT, 1, SMALL>(P, s);
+  if (cols <= 16) return launch<FMT, 2, SMALL>(P, s);
+  return launch<FMT, 4, SMALL>(P, s);
 }
 
 }  // namespace gv
@@ -753,10 +791,14 @@ cudaError_t launch_gemv(int fmt, const void* x, int x_bf16, int m, const uint8_t
   const gv::Params P{x, codes, scales, static_cast<const uint16_t*>(zeros), tscale, y, n, m, k,
                      (k + 127) / 128, x_bf16, y_bf16, 0, 0, 1, 0, 0, 1, 0, 0, 0};
   switch (fmt) {
-    case KQ_FMT_INT4_SYM: return gv::launch_tiles<KQ_FMT_INT4_SYM>(P, s);
-    case KQ_FMT_INT4_ASYM: return gv::launch_tiles<KQ_FMT_INT4_ASYM>(P, s);
-    case KQ_FMT_NVFP4: return gv::launch_tiles<KQ_FMT_NVFP4>(P, s);
-    default: return gv::launch_tiles<KQ_FMT_MXFP4>(P, s);
+    case KQ_FMT_INT4_SYM:
+      return y_bf16 ? gv::launch_tiles<KQ_FMT_INT4_SYM, true>(P, s)
+                    : gv::launch_tiles<KQ_FMT_INT4_SYM, false>(P, s);
+    case KQ_FMT_INT4_ASYM:
+      return y_bf16 ? gv::launch_tiles<KQ_FMT_INT4_ASYM, true>(P, s)
+                    : gv::launch_tiles<KQ_FMT_INT4_ASYM, false>(P, s);
+    case KQ_FMT_NVFP4: return gv::launch_tiles<KQ_FMT_NVFP4, false>(P, s);
+    default: return gv::launch_tiles<KQ_FMT_MXFP4, false>(P, s);
   }
 }
 
