@@ -50,18 +50,19 @@ namespace cg = cooperative_groups;
 using sm100::pow2f;
 
 // A warp streams its rows in steps of 16 rows by kStep groups, kStages of which are
-// on their way or in use.  Up to two tiles of 8 columns: two CTAs of 8 warps an
-// SM.  Four tiles: one CTA of 16 warps, which stages x once an SM.
-constexpr int kStep = 4;
-constexpr int kStages = 2;
-constexpr int kRow = kStep * 64;                  // bytes of a staged row of codes
-constexpr int kScaleRow = kStep * 8;              // bytes of its scales at most
-constexpr int kStage = 16 * (kRow + kScaleRow);
+// on their way or in use.  One tile of 8 columns: two CTAs of 8 warps an SM.  More:
+// one CTA of 16 warps, which stages x once an SM, and shorter steps, which leave x
+// and the sums more room (32000 x 4096 by 16 tokens took 79 us with two CTAs).
 template <int NT>
 struct Shape {
-  static constexpr int kWarps = NT == 4 ? 16 : 8;
+  static constexpr int kWarps = NT == 1 ? 8 : 16;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCtas = NT == 4 ? 1 : 2;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;
+  static constexpr int kStep = NT == 1 ? 4 : 2;
+  static constexpr int kStages = NT == 1 ? 2 : 3;
+  static constexpr int kRow = kStep * 64;             // bytes of a staged row of codes
+  static constexpr int kScaleRow = kStep * 8;         // bytes of its scales at most
+  static constexpr int kStage = 16 * (kRow + kScaleRow);
 };
 
 struct Params {
@@ -74,7 +75,7 @@ struct Params {
   int64_t n;
   int m, k, groups;                       // groups of 128 columns, the last may be short
   int x_bf16, y_bf16;
-  int tiles;                              // 16-row tiles of a cluster
+  int tiles, round;                       // 16-row tiles of a cluster, and of a round
   int seg;                                // groups whose x is staged at a time
   int parts, part_shift, part;            // warps that share a tile's groups: 2^part_shift, steps
                                           // of each
@@ -286,21 +287,24 @@ __device__ __forceinline__ int piece(int r, int c) {
 }
 
 // A warp's stream through the codes: the rows it is at, and the lane's share of
-// the copies of a step (16 lanes a row, 2 rows at a time).
-template <int FMT, bool BLOCKS>
+// the copies of a step (4 kStep lanes a row).
+template <int FMT, int NT>
 struct Stream {
+  using S = Shape<NT>;
+  static constexpr bool BLOCKS = kByBlock<FMT, NT>;
+  static constexpr int LANES = 4 * S::kStep, ROWS = 32 / LANES;   // lanes a row, rows at a time
   const uint8_t* codes;                   // row0, the lane's piece
   const uint8_t* scales;                  // the lane's row of scales (zero points)
-  int off[8];                             // bytes to the lane's rows (the last row again behind it)
+  int off[16 / ROWS];                     // bytes to the lane's rows (the last row again behind it)
   int64_t row0;
 
   __device__ __forceinline__ void start(const Params& P, int64_t row) {
     const int lane = threadIdx.x & 31;
     const int left = (int)min(P.n - 1 - row, (int64_t)15);
     row0 = row;
-    codes = P.codes + row * (P.k / 2) + 16 * (lane & 15);
+    codes = P.codes + row * (P.k / 2) + 16 * (lane % LANES);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) off[i] = min(left, 2 * i + (lane >> 4)) * (P.k / 2);
+    for (int i = 0; i < 16 / ROWS; ++i) off[i] = min(left, ROWS * i + lane / LANES) * (P.k / 2);
     const int64_t sr = row + min(left, lane & 15);
     if (FMT == KQ_FMT_INT4_ASYM)
       scales = reinterpret_cast<const uint8_t*>(
@@ -315,22 +319,25 @@ struct Stream {
   // behind them 16 rows of scales: INT4 asymmetric kStep fp16 scales and zero
   // points, NVFP4 8 E4M3 bytes a group, MXFP4 4 E8M0 bytes a group.
   __device__ __forceinline__ void copy(const Params& P, int g0, int gend, uint8_t* stage) const {
-    const int lane = threadIdx.x & 31, c = lane & 15, r = lane >> 4;
+    constexpr int kStep = S::kStep;
+    const int lane = threadIdx.x & 31, c = lane % LANES, r = lane / LANES;
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(stage);
     const bool in = g0 + (c >> 2) < gend && g0 * 128 + 32 * c < P.k;
     const uint8_t* from = codes + (in ? g0 * 64 : 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      copy_async<16>(to + (2 * i + r) * kRow + piece<BLOCKS>(2 * i + r, c), from + off[i], in);
+    for (int i = 0; i < 16 / ROWS; ++i)
+      copy_async<16>(to + (ROWS * i + r) * S::kRow + piece<BLOCKS>(ROWS * i + r, c), from + off[i],
+                     in);
     if (FMT == KQ_FMT_INT4_SYM) return;
-    const uint32_t ts = to + 16 * kRow + (lane & 15) * kScaleRow;
+    const uint32_t ts = to + 16 * S::kRow + (lane & 15) * S::kScaleRow;
     if (P.wide) {
       if (FMT == KQ_FMT_INT4_ASYM)
-        copy_async<8>(ts + (lane >> 4) * 8, scales + 2 * g0);
-      else if (FMT == KQ_FMT_NVFP4)
-        copy_async<16>(ts + (lane >> 4) * 16, scales + 8 * g0);
-      else if (lane < 16)
-        copy_async<16>(ts, scales + 4 * g0);
+        copy_async<2 * kStep>(ts + (lane >> 4) * 2 * kStep, scales + 2 * g0);
+      else if (FMT == KQ_FMT_NVFP4) {
+        if (lane < 8 * kStep) copy_async<16>(ts + (lane >> 4) * 16, scales + 8 * g0);
+      } else if (lane < 16) {
+        copy_async<4 * kStep>(ts, scales + 4 * g0);
+      }
       return;
     }
     // scales that no aligned copy reaches: one by one
@@ -341,7 +348,7 @@ struct Stream {
       const int row = i / (kStep * per), e = i - row * (kStep * per), at = g0 * per + e;
       const int64_t src = (row0 + min(left, row)) * count + at;
       const bool ok = at < gend * per && at < count;
-      uint8_t* d = stage + 16 * kRow + row * kScaleRow;
+      uint8_t* d = stage + 16 * S::kRow + row * S::kScaleRow;
       if (FMT == KQ_FMT_INT4_ASYM) {
         reinterpret_cast<uint16_t*>(d)[e] =
             ok ? __ldg(static_cast<const uint16_t*>(P.scales) + src) : 0;
@@ -359,6 +366,8 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
                                              const float2* xf, float (&acc)[NT][4]) {
   constexpr bool INT4 = FMT == KQ_FMT_INT4_SYM || FMT == KQ_FMT_INT4_ASYM;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  using S = Shape<NT>;
+  constexpr int kStep = S::kStep, kRow = S::kRow, kScaleRow = S::kScaleRow;
   constexpr bool BLOCKS = kByBlock<FMT, NT>;
   const uint8_t* ca = stage + g * kRow;
   const uint8_t* sca = stage + 16 * kRow + g * kScaleRow;
@@ -530,142 +539,156 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   using S = Shape<NT>;
   constexpr bool INT4 = FMT == KQ_FMT_INT4_SYM || FMT == KQ_FMT_INT4_ASYM;
   constexpr bool BLOCKS = kByBlock<FMT, NT>;
-  constexpr int kWarps = S::kWarps;
+  constexpr bool SUMS = FMT == KQ_FMT_INT4_ASYM || (FMT == KQ_FMT_INT4_SYM && SMALL);
+  constexpr int kWarps = S::kWarps, kStep = S::kStep, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   const int ranks = P.ranks, rank = ranks > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * (kStages * kStage);
-  uint4* xs = reinterpret_cast<uint4*>(smem + kWarps * kStages * kStage);
+  uint8_t* ring = smem + warp * (kStages * S::kStage);
+  uint4* xs = reinterpret_cast<uint4*>(smem + kWarps * kStages * S::kStage);
   float2* xf = reinterpret_cast<float2*>(xs + P.seg * NT * 128);
   float* red = reinterpret_cast<float*>(xf + P.seg * NT * 8);
   // the others' shared memory may be written once they have all started
   if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   bool started = ranks == 1;
-  const int64_t row0 = (int64_t)(blockIdx.x >> P.rank_shift) * P.tiles * 16;
-  const int tiles = (int)min((int64_t)P.tiles, (P.n - row0 + 15) >> 4);
-  const int own = (P.tiles + ranks - 1) >> P.rank_shift;  // tiles a CTA owns at most
+  const int64_t first_row = (int64_t)(blockIdx.x >> P.rank_shift) * P.tiles * 16;
+  const int all_tiles = (int)min((int64_t)P.tiles, (P.n - first_row + 15) >> 4);
+  const int own = (P.round + ranks - 1) >> P.rank_shift;  // tiles of a round a CTA owns at most
   const int mt = P.m, parts = P.parts;
   const int gbegin = rank_begin(P, rank), gend = rank_begin(P, rank + 1);
-  for (int g0 = gbegin; g0 < gend; g0 += P.seg) {
-    const int ng = min(P.seg, gend - g0), steps = (ng + kStep - 1) / kStep;
-    // a warp's units: every kWarps-th (tile, part); a part is P.part steps
-    struct Unit {
-      int tile, part;
-    };
-    const Unit begin{warp >> P.part_shift, warp & (parts - 1)};
-    auto next = [&](Unit& u) {
-      u.tile += kWarps >> P.part_shift;
-      u.part += kWarps & (parts - 1);
-      if (u.part >= parts) {
-        u.part -= parts;
-        ++u.tile;
-      }
-    };
-    Unit fu = begin;                      // copied next
-    int fstep = 0, fend = 0, fill = 0;
-    Stream<FMT, BLOCKS> stream;
-    auto open = [&] {
-      for (; fu.tile < tiles; next(fu)) {
-        fstep = fu.part * P.part;
-        fend = min(fstep + P.part, steps);
-        if (fstep < fend) {
-          stream.start(P, row0 + 16 * fu.tile);
-          return;
+  // rounds: as many tiles as the sums have room for
+  for (int t0 = 0; t0 < all_tiles; t0 += P.round) {
+    const int tiles = min(P.round, all_tiles - t0);
+    const int64_t row0 = first_row + 16 * (int64_t)t0;
+    for (int g0 = gbegin; g0 < gend; g0 += P.seg) {
+      // x stays staged from round to round where it is in one piece
+      const bool fresh = t0 == 0 || gend - gbegin > P.seg;
+      const int ng = min(P.seg, gend - g0), steps = (ng + kStep - 1) / kStep;
+      // a warp's units: every kWarps-th (tile, part); a part is P.part steps
+      struct Unit {
+        int tile, part;
+      };
+      const Unit begin{warp >> P.part_shift, warp & (parts - 1)};
+      auto next = [&](Unit& u) {
+        u.tile += kWarps >> P.part_shift;
+        u.part += kWarps & (parts - 1);
+        if (u.part >= parts) {
+          u.part -= parts;
+          ++u.tile;
         }
-      }
-    };
-    auto fetch = [&] {
-      if (fu.tile < tiles) {
-        stream.copy(P, g0 + fstep * kStep, g0 + ng, ring + fill * kStage);
-        if (++fill == kStages) fill = 0;
-        if (++fstep == fend) {
-          next(fu);
-          open();
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    const Eight x0 = load_x<NT>(P, g0, ng, 0);
-    open();
-#pragma unroll 1
-    for (int i = 0; i < kStages; ++i) fetch();
-    if (g0 > gbegin) __syncthreads();     // the last segment's x is no longer read
-    constexpr bool SUMS = FMT == KQ_FMT_INT4_ASYM || (FMT == KQ_FMT_INT4_SYM && SMALL);
-    stage_x<SMALL, SUMS, BLOCKS, INT4, NT>(P, g0, ng, x0, xs, xf);
-    __syncthreads();
-    if (!started) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    started = true;
-    int stage = 0;
-#pragma unroll 1
-    for (Unit u = begin; u.tile < tiles; next(u)) {
-      const int tile = u.tile, part = u.part;
-      const int s0 = part * P.part, s1 = min(s0 + P.part, steps);
-      float acc[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
-#pragma unroll 1
-      for (int step = s0; step < s1; ++step) {
-        asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
-        __syncwarp();
-        compute_step<FMT, NT, SMALL>(ring + stage * kStage, step * kStep, ng - step * kStep, xs, xf, acc);
-        __syncwarp();                     // the stage is free
-        if (++stage == kStages) stage = 0;
-        fetch();
-      }
-      const int owner = tile & (ranks - 1);
-      float* to = red + (((rank * parts + part) * own + (tile >> P.rank_shift)) * 16 + g) * mt;
-      if (owner != rank) to = cg::this_cluster().map_shared_rank(to, owner);
-      // behind the first segment: on top of what the same lane put there
-      auto put = [&](float* at, float v) { *at = g0 > gbegin ? *at + v : v; };
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (P.x_bf16) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tok = 8 * n + 2 * t + (e & 1);
-            if (tok < mt) put(to + 8 * (e >> 1) * mt + tok, acc[n][e]);
+      };
+      Unit fu = begin;                      // copied next
+      int fstep = 0, fend = 0, fill = 0;
+      Stream<FMT, NT> stream;
+      auto open = [&] {
+        for (; fu.tile < tiles; next(fu)) {
+          fstep = fu.part * P.part;
+          fend = min(fstep + P.part, steps);
+          if (fstep < fend) {
+            stream.start(P, row0 + 16 * fu.tile);
+            return;
           }
-        } else {
-          const int tok = 4 * n + t;
-          if (tok < mt) {
-            put(to + tok, acc[n][0] + acc[n][1]);
-            put(to + 8 * mt + tok, acc[n][2] + acc[n][3]);
+        }
+      };
+      auto fetch = [&] {
+        if (fu.tile < tiles) {
+          stream.copy(P, g0 + fstep * kStep, g0 + ng, ring + fill * S::kStage);
+          if (++fill == kStages) fill = 0;
+          if (++fstep == fend) {
+            next(fu);
+            open();
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      Eight x0{};
+      if (fresh) x0 = load_x<NT>(P, g0, ng, 0);
+      open();
+#pragma unroll 1
+      for (int i = 0; i < kStages; ++i) fetch();
+      if (fresh) {
+        if (t0 > 0 || g0 > gbegin) __syncthreads();   // the last segment's x is no longer read
+        stage_x<SMALL, SUMS, BLOCKS, INT4, NT>(P, g0, ng, x0, xs, xf);
+        __syncthreads();
+      }
+      if (!started) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      started = true;
+      int stage = 0;
+#pragma unroll 1
+      for (Unit u = begin; u.tile < tiles; next(u)) {
+        const int tile = u.tile, part = u.part;
+        const int s0 = part * P.part, s1 = min(s0 + P.part, steps);
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
+#pragma unroll 1
+        for (int step = s0; step < s1; ++step) {
+          asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
+          __syncwarp();
+          compute_step<FMT, NT, SMALL>(ring + stage * S::kStage, step * kStep, ng - step * kStep, xs, xf, acc);
+          __syncwarp();                     // the stage is free
+          if (++stage == kStages) stage = 0;
+          fetch();
+        }
+        const int owner = tile & (ranks - 1);
+        float* to = red + (((rank * parts + part) * own + (tile >> P.rank_shift)) * 16 + g) * mt;
+        if (owner != rank) to = cg::this_cluster().map_shared_rank(to, owner);
+        // behind the first segment: on top of what the same lane put there
+        auto put = [&](float* at, float v) { *at = g0 > gbegin ? *at + v : v; };
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (P.x_bf16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tok = 8 * n + 2 * t + (e & 1);
+              if (tok < mt) put(to + 8 * (e >> 1) * mt + tok, acc[n][e]);
+            }
+          } else {
+            const int tok = 4 * n + t;
+            if (tok < mt) {
+              put(to + tok, acc[n][0] + acc[n][1]);
+              put(to + 8 * mt + tok, acc[n][2] + acc[n][3]);
+            }
           }
         }
       }
     }
+    auto meet = [&] {
+      if (ranks > 1) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      } else {
+        __syncthreads();
+      }
+    };
+    meet();
+    // ---- join: the ranks' and parts' sums in order; a warp takes a tile by two tokens,
+    // a lane a row
+    const int mine = (tiles - rank + ranks - 1) >> P.rank_shift;    // tiles this CTA owns
+    const int pairs = (mt + 1) >> 1, slots = ranks * parts, pitch = own * 16 * mt;
+    const float t_scale = FMT == KQ_FMT_NVFP4 ? __ldg(P.tscale) : 1.0f;
+    for (int q = warp; q < mine * pairs; q += kWarps) {
+      const int tl = q / pairs, tok = 2 * (q - tl * pairs) + (lane >> 4), r = lane & 15;
+      const int64_t row = row0 + ((tl << P.rank_shift) + rank) * 16 + r;
+      if (tok >= mt || row >= P.n) continue;
+      const float* from = red + (tl * 16 + r) * mt + tok;
+      float v = 0.0f;
+#pragma unroll 8
+      for (int c = 0; c < slots; ++c) v += from[c * pitch];
+      if (SMALL) v *= 0x1p24f;              // the codes' 2^-24
+      if (FMT == KQ_FMT_INT4_SYM) v *= __ldg(static_cast<const float*>(P.scales) + row);
+      if (FMT == KQ_FMT_NVFP4) v *= t_scale;
+      const int64_t at = tok * P.n + row;
+      if (P.y_bf16)
+        static_cast<__nv_bfloat16*>(P.y)[at] = __float2bfloat16_rn(v);
+      else
+        static_cast<float*>(P.y)[at] = v;
+    }
+    if (t0 + P.round < all_tiles) meet();   // the sums are read: the next round's may come
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if (ranks > 1) {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  } else {
-    __syncthreads();
-  }
-  // ---- join: the ranks' and parts' sums in order; a warp takes a tile by two tokens,
-  // a lane a row
-  const int mine = (tiles - rank + ranks - 1) >> P.rank_shift;    // tiles this CTA owns
-  const int pairs = (mt + 1) >> 1, slots = ranks * parts, pitch = own * 16 * mt;
-  const float t_scale = FMT == KQ_FMT_NVFP4 ? __ldg(P.tscale) : 1.0f;
-  for (int q = warp; q < mine * pairs; q += kWarps) {
-    const int tl = q / pairs, tok = 2 * (q - tl * pairs) + (lane >> 4), r = lane & 15;
-    const int64_t row = row0 + ((tl << P.rank_shift) + rank) * 16 + r;
-    if (tok >= mt || row >= P.n) continue;
-    const float* from = red + (tl * 16 + r) * mt + tok;
-    float v = 0.0f;
-#pragma unroll 8
-    for (int c = 0; c < slots; ++c) v += from[c * pitch];
-    if (SMALL) v *= 0x1p24f;              // the codes' 2^-24
-    if (FMT == KQ_FMT_INT4_SYM) v *= __ldg(static_cast<const float*>(P.scales) + row);
-    if (FMT == KQ_FMT_NVFP4) v *= t_scale;
-    const int64_t at = tok * P.n + row;
-    if (P.y_bf16)
-      static_cast<__nv_bfloat16*>(P.y)[at] = __float2bfloat16_rn(v);
-    else
-      static_cast<float*>(P.y)[at] = v;
-  }
 }
 
 // CTAs that split k.  8 took the 4096 x 4096 product of one token from 6.3 to 6.6 us
@@ -676,10 +699,11 @@ constexpr int kSplit = 4;
 // Shared memory of a CTA: the stages, x of a segment, the sums.
 template <int NT>
 struct Room {
-  static constexpr int kAll = (Shape<NT>::kCtas == 1 ? 227 : 113) * 1024;
-  static constexpr int kRings = Shape<NT>::kWarps * kStages * kStage;
-  static constexpr int kSums = 12 * 1024;
-  static constexpr int kGroups = (kAll - kRings - kSums) / (NT * (2048 + 64)) / kStep * kStep;
+  using S = Shape<NT>;
+  static constexpr int kAll = (S::kCtas == 1 ? 227 : 113) * 1024;
+  static constexpr int kRings = S::kWarps * S::kStages * S::kStage;
+  static constexpr int kSums = (NT == 1 ? 12 : 20) * 1024;
+  static constexpr int kGroups = (kAll - kRings - kSums) / (NT * (2048 + 64)) / S::kStep * S::kStep;
   static_assert(kGroups >= 4, "room for x");
 };
 
@@ -721,6 +745,7 @@ cudaError_t resident_ctas(int ranks, int* out) {
 template <int FMT, int NT, bool SMALL>
 cudaError_t launch(Params P, cudaStream_t s) {
   using R = Room<NT>;
+  constexpr int kStep = Shape<NT>::kStep;
   int ranks = 1;
   while (ranks < kSplit && P.groups / (2 * ranks) >= kStep) ranks *= 2;
   while (ranks < 8 && P.groups > ranks * R::kGroups) ranks *= 2;
@@ -739,18 +764,22 @@ cudaError_t launch(Params P, cudaStream_t s) {
   // row begins at a multiple of kStep groups
   const uintptr_t at = reinterpret_cast<uintptr_t>(P.scales) | reinterpret_cast<uintptr_t>(P.zeros);
   P.wide = P.groups % (kStep * ranks) == 0 && P.k % 128 == 0 &&
-           at % (FMT == KQ_FMT_INT4_ASYM ? 8 : 16) == 0;
-  // rows for one round of CTAs, as far as their sums fit
-  int64_t tiles = (all + ctas / ranks - 1) / (ctas / ranks);
-  const int64_t room = R::kSums / (P.m * 64);           // tiles times parts, and a rank's rounding
-  if (tiles > room - ranks + 1) tiles = room - ranks + 1;
-  P.tiles = (int)(tiles < 1 ? 1 : tiles);
+           at % (FMT == KQ_FMT_INT4_ASYM ? 2 * kStep : FMT == KQ_FMT_NVFP4 ? 16 : 4 * kStep) == 0;
+  // rows for as many clusters as run at a time, in rounds as far as their sums fit
+  const int clusters = ctas / ranks;
+  P.tiles = (int)((all + clusters - 1) / clusters);
+  const int room = R::kSums / (P.m * 64);               // tiles times parts, and a rank's rounding
+  P.round = P.tiles;
+  if (P.round > room - ranks + 1) {
+    const int rounds = (P.tiles + room - ranks) / (room - ranks + 1);
+    P.round = (P.tiles + rounds - 1) / rounds;
+  }
   // parts: the shortest way through the units for the CTA's warps
-  const int steps = P.seg / kStep, own = (P.tiles + ranks - 1) / ranks;
+  const int steps = P.seg / kStep, own = (P.round + ranks - 1) / ranks;
   int best = 1 << 30;
   for (int shift = 0, p = 1; (shift == 0 || p <= steps) && p * own * ranks <= room; ++shift, p *= 2) {
-    const int rounds = (P.tiles * p + Shape<NT>::kWarps - 1) / Shape<NT>::kWarps;
-    const int part = (steps + p - 1) / p, way = rounds * part;
+    const int turns = (P.round * p + Shape<NT>::kWarps - 1) / Shape<NT>::kWarps;
+    const int part = (steps + p - 1) / p, way = turns * part;
     if (way < best) {
       best = way;
       P.parts = p;
@@ -789,7 +818,7 @@ cudaError_t launch_gemv(int fmt, const void* x, int x_bf16, int m, const uint8_t
                         const void* scales, const void* zeros, const float* tscale, int64_t n,
                         int k, void* y, int y_bf16, cudaStream_t s) {
   const gv::Params P{x, codes, scales, static_cast<const uint16_t*>(zeros), tscale, y, n, m, k,
-                     (k + 127) / 128, x_bf16, y_bf16, 0, 0, 1, 0, 0, 1, 0, 0, 0};
+                     (k + 127) / 128, x_bf16, y_bf16, 0, 0, 0, 1, 0, 0, 1, 0, 0, 0};
   switch (fmt) {
     case KQ_FMT_INT4_SYM:
       return y_bf16 ? gv::launch_tiles<KQ_FMT_INT4_SYM, true>(P, s)
