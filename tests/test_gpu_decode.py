@@ -582,3 +582,141 @@ def test_decode_step_together():
     y = torch.empty((3, n), device="cuda")
     _gemv("int4_asym", rot, *w, y)
     _check_gemv("int4_asym", rot.double().cpu().numpy(), w, y)
+
+
+# ------------------------------------------- where the kernels change their ways
+def _check_some_rows(fmt, x, w, y, rows):
+    codes, scales, zeros, t = w
+    part = (codes[rows], scales[rows], None if zeros is None else zeros[rows], t)
+    _check_gemv(fmt, x, part, y[:, torch.from_numpy(rows).cuda()])
+
+
+@pytest.mark.parametrize("fmt,n,k,m,xt,yt", [
+    # more tiles than a round's sums have room for: one CTA a cluster, four of them
+    ("int4_asym", 60011, 128, 16, "bf16", "f32"), ("int4_sym", 52001, 256, 8, "bf16", "bf16"),
+    ("nvfp4", 12007, 2048, 16, "bf16", "bf16"), ("mxfp4", 11003, 2048, 16, "f32", "f32"),
+    # x in several segments, and rounds on top of them
+    ("int4_sym", 4801, 13312, 16, "f32", "f32"), ("int4_asym", 100, 32768, 16, "f32", "f32"),
+    ("mxfp4", 33, 131072, 3, "bf16", "f32"), ("nvfp4", 70, 65536 + 160, 9, "bf16", "f32"),
+])
+def test_gemv_rounds_and_segments(fmt, n, k, m, xt, yt):
+    rng = np.random.default_rng(n + k)
+    w = _weights(rng, fmt, n, k)
+    x = torch.from_numpy(rng.standard_normal((m, k))).cuda().to(KIND[xt])
+    y = torch.full((m, n), float("nan"), dtype=KIND[yt], device="cuda")
+    _gemv(fmt, x, *w, y)
+    rows = np.unique(np.concatenate([np.arange(min(n, 20)), rng.integers(0, n, 200),
+                                     np.arange(max(0, n - 40), n)]))
+    _check_some_rows(fmt, x.double().cpu().numpy(), w, y, rows)
+    assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("fmt", ["int4_asym", "nvfp4", "mxfp4"])
+def test_gemv_scales_at_other_alignments(fmt):
+    """Scales that begin off the 16-byte grid, as a layer's slice of a larger tensor
+    may: the result is that of aligned copies."""
+    rng = np.random.default_rng(3)
+    codes, scales, zeros, t = _weights(rng, fmt, 65, 1024)
+    x = torch.from_numpy(rng.standard_normal((2, 1024))).cuda().bfloat16()
+    want = torch.empty((2, 65), device="cuda")
+    _gemv(fmt, x, codes, scales, zeros, t, want)
+
+    def moved(a, by):
+        flat = torch.zeros(a.size + by, dtype=torch.from_numpy(a).dtype, device="cuda")
+        flat[by:] = _dev(a).view(-1)
+        return flat[by:].view(a.shape)
+    for by in (1, 2, 3) if fmt != "nvfp4" else (2, 4, 6):
+        y = torch.empty((2, 65), device="cuda")
+        kq.kq_gemv(FMT[fmt], x, _dev(oracle.pack_nibbles(codes)), moved(scales, by),
+                   None if zeros is None else moved(zeros, by),
+                   None if t is None else torch.tensor([float(t)], device="cuda"),
+                   128 if zeros is not None else 0, y)
+        assert torch.equal(y, want)
+
+
+def test_gemv_streams_and_graph():
+    rng = np.random.default_rng(4)
+    w = _weights(rng, "int4_asym", 300, 1024)
+    codes, s, z = _dev(oracle.pack_nibbles(w[0])), _dev(w[1]), _dev(w[2])
+    xs = [torch.from_numpy(rng.standard_normal((4, 1024))).cuda().bfloat16() for _ in range(2)]
+    want = [torch.empty((4, 300), device="cuda") for _ in range(2)]
+    for x, y in zip(xs, want):
+        kq.kq_gemv(kq.KQ_FMT_INT4_ASYM, x, codes, s, z, None, 128, y)
+    torch.cuda.synchronize()
+    # two calls at once, on streams of their own
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [torch.empty((4, 300), device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, y, st in zip(xs, got, streams):
+            kq.kq_gemv(kq.KQ_FMT_INT4_ASYM, x, codes, s, z, None, 128, y, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # captured, then replayed on an input changed in place
+    x, y = xs[0].clone(), torch.empty((4, 300), device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kq.kq_gemv(kq.KQ_FMT_INT4_ASYM, x, codes, s, z, None, 128, y)
+    x.copy_(xs[1])
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[1])
+
+
+def test_attention_calls_at_once():
+    """Two streams, a workspace each: neither sees the other."""
+    page = 16
+    cases = [_case(30 + i, lens, 8, 4, page) for i, lens in enumerate([[3000], [5, 700, 40]])]
+    args = []
+    for q, k, v, ks, vs, table, lens in cases:
+        args.append((q, _upload(k), _upload(v), _dev(ks), _dev(vs), _dev(table), page, _dev(lens), 0.1))
+    want = [_attn(*a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    ws = [kq.empty_attn_workspace(a[0].shape[0], 32, 8) for a in args]
+    out = [torch.empty_like(a[0]) for a in args]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, w, o, st in zip(args, ws, out, streams):
+            _attn(*a, ws=w, out=o, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_attention_joins_many_rows_and_few():
+    """The three ways partial sums are joined (by the number of rows), every
+    sequence split over several CTAs."""
+    _whole(40, [2000, 1990], 8, 8, 16)                       # 128 rows
+    _whole(41, [700 + i for i in range(24)], 8, 4, 16)       # 768 rows
+    _whole(42, [400 + i for i in range(40)], 8, 5, 16)       # 1600 rows
+    _whole(43, [3000, 10, 0], 1, 3, 16)
+
+
+def test_cache_offsets_past_32_bits():
+    """Rows whose codes begin behind 2^32 bytes: attention and page copies."""
+    heads, page = 32, 16
+    slots = (1 << 32) // (heads * 64) + 4 * page
+    rng = np.random.default_rng(50)
+    caches = [kq.empty_kv_cache(slots, heads * 128) for _ in range(2)]
+    pages = slots // page
+    table = np.array([[pages - 1, 3, pages - 2]], dtype=np.int32)
+    small = []
+    for c in caches:
+        codes, scales, zeros = _cache(rng, 3 * page, heads)
+        for i, p in enumerate(table[0]):
+            at, here = slice(int(p) * page, int(p) * page + page), slice(i * page, i * page + page)
+            c.codes[at] = _dev(oracle.pack_nibbles(codes[here]))
+            c.scales[at], c.zeros[at] = _dev(scales[here]), _dev(zeros[here])
+        small.append((codes, scales, zeros))
+    q = torch.from_numpy(rng.standard_normal((1, heads, 128))).cuda().bfloat16()
+    lens = np.array([45], dtype=np.int32)
+    out = _attn(q, *caches, None, None, _dev(table), page, _dev(lens), 0.1)
+    _check_attn(out, q.double().cpu().numpy(), *small, None, None,
+                np.array([[0, 1, 2]]), page, lens, 0.1, 0, 0)
+    kq.kq_kv_copy_pages(_dev(np.array([[pages - 1, pages - 4], [3, pages - 3]], dtype=np.int32)),
+                        page, *caches)
+    for c in caches:
+        for a in (c.codes, c.scales, c.zeros):
+            a = a.view(torch.uint8).view(slots, -1)
+            for s, d in ((pages - 1, pages - 4), (3, pages - 3)):
+                assert torch.equal(a[s * page:(s + 1) * page], a[d * page:(d + 1) * page])
