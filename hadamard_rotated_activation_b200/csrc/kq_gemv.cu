@@ -27,11 +27,17 @@
 // fp32 rows are two columns, the rounded value and 2^11 times what it leaves.
 // A group's sum leaves the tensor core after 8 steps and is added in fp32.
 //
-// Bound by HBM: every code is read once, m n k multiplications ride along.  One
-// CTA takes R rows (16 a warp) and a range of k; the CTAs of a cluster share the
-// rows, split k between them and join their sums through distributed shared
-// memory in rank order, so there is no workspace, one launch and a fixed order
-// of additions.
+// Bound by HBM: every code is read once, m n k multiplications ride along.  The
+// CTAs of a cluster share the rows, split k between them and join their sums through
+// distributed shared memory in a fixed order, so there is no workspace and one
+// launch.  Measured (one B200, time between calls in a graph), INT4 asymmetric:
+// 4096 x 4096 by 1 token 5.2 us, 12288 x 4096 by 8 tokens 12.0 us; MXFP4 32003 x 4096
+// by 4 tokens 22.4 us = 3.1 TB/s; NVFP4 4096 x 12288 by 2 fp32 tokens 10.0 us.  Of
+// the 12.0 us about 2 are the launch, 1 the start, 2 staging x (which every CTA does
+// for its range of k), 4 the products at 1.9 instructions a cycle, 1 the cluster
+// barrier and 0.7 the join; with no copies at all it still takes 10.9.  Of the 22.4 us
+// 15.5 remain without the products, so there the memory and the instructions of the
+// E2M1 conversion and the block scales (about 120 a group and warp) share the bound.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -711,7 +717,6 @@ struct Room {
 // stays within a GPC, so it is less than all SMs hold.  Looked up once.
 template <int FMT, int NT, bool SMALL>
 cudaError_t resident_ctas(int ranks, int* out) {
-  // the attribute set here holds for every launch of this kernel on the device
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices][4];
   int dev = 0;
@@ -790,6 +795,9 @@ cudaError_t launch(Params P, cudaStream_t s) {
   const size_t smem = R::kRings + (size_t)P.seg * NT * (2048 + 64) +
                       sizeof(float) * ranks * P.parts * own * 16 * P.m;
   if (smem > (size_t)R::kAll) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute((const void*)k_gemv<FMT, NT, SMALL>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, R::kAll);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((all + P.tiles - 1) / P.tiles * ranks));
   cfg.blockDim = dim3(Shape<NT>::kThreads);

@@ -311,8 +311,11 @@ KQ_API kq_status kq_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* a_scales,
  * discrete_descent's note: INT4-g128, NVFP4 and MXFP4 weights):
  *   y[j][i] = sum_k x[j][k] w[i][k],
  * where w is what kq_dequant defines for the same fmt, codes, scales, zeros,
- * tensor_scale and group.  No weight is rounded on the way (code times scale
- * is exact in the arithmetic used); products are accumulated in fp32.
+ * tensor_scale and group.  Products are accumulated in fp32; no weight is
+ * rounded on the way, except MXFP4 blocks more than 2^23 below the largest of
+ * their row's group of 128 columns when there are more than 8 columns (tokens of
+ * bf16, or twice the tokens of fp32).  INT4 products for a bf16 y keep about 17
+ * bits of their largest, all others about 22.
  *   x       [m, k] fp32 or bf16 (x_dtype), 0 <= m <= KQ_GEMV_MAX_TOKENS; m == 0
  *           is a no-op.  fp32 rows keep 22 significant bits.
  *   codes   [n, k/2] bytes; scales, zeros, tensor_scale: as for kq_dequant with
