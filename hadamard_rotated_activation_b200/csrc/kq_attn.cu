@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_wide(AttnArgs P, int g
       sum = fmaf(f, red[k][threadIdx.x], sum);
       ls = fmaf(f, wl[k], ls);
     }
-    red[0][threadIdx.x] = ls > 0.0f ? sum / ls : 0.0f;
+    red[0][threadIdx.x] = ls == 0.0f ? 0.0f : sum / ls;
   }
   __syncthreads();
   if (warp == 0) store_row(P, red[0], b, qh, kh);

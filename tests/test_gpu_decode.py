@@ -720,3 +720,20 @@ def test_cache_offsets_past_32_bits():
             a = a.view(torch.uint8).view(slots, -1)
             for s, d in ((pages - 1, pages - 4), (3, pages - 3)):
                 assert torch.equal(a[s * page:(s + 1) * page], a[d * page:(d + 1) * page])
+
+
+@pytest.mark.parametrize("batch", [2, 20, 40])
+def test_attention_nan_query_stays_in_its_head(batch):
+    """A NaN in one head's query reaches all of that head's result and nothing
+    else, whichever way the partial sums are joined (by the number of rows)."""
+    q, k, v, ks, vs, table, lens = _case(33, [9, 700] + [650] * (batch - 2), 8, 4, 16)
+    bad = q.clone()
+    for b, h in ((0, 3), (1, 5), (batch - 1, 31)):
+        q[b, h, 7] = 0
+        bad[b, h, 7] = float("nan")
+    clean = _run_case(q, k, v, ks, vs, table, lens, 16, 128 ** -0.5)
+    out = _run_case(bad, k, v, ks, vs, table, lens, 16, 128 ** -0.5)
+    for b, h in ((0, 3), (1, 5), (batch - 1, 31)):
+        assert out[b, h].isnan().all()
+        out[b, h] = clean[b, h]
+    _check_attn(out, q.double().cpu().numpy(), k, v, ks, vs, table, 16, lens, 128 ** -0.5, 0, 0)
