@@ -307,6 +307,8 @@ def _want(t, what: str, dtype, shape, index: int) -> int:
     """Device pointer of a contiguous tensor of this type and shape on device
     `index`; ValueError for anything else.  The kernels take sizes from the
     shapes, so a wrong one would read or write out of bounds."""
+    if t is None:
+        raise ValueError(f"{what}: missing")
     if t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 \
             and t.is_contiguous():
         return t.data_ptr()
@@ -318,6 +320,13 @@ def _want(t, what: str, dtype, shape, index: int) -> int:
     if not t.is_contiguous():
         raise ValueError(f"{what}: kq functions take contiguous tensors")
     raise ValueError(f"{what}: on cuda:{t.get_device()}, the call's tensors are on cuda:{index}")
+
+
+def _int32(**sizes) -> None:
+    """ValueError for a size that the C entry's 32 bits would cut."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name}: {v} does not fit 32 bits")
 
 
 def _launch(fn, where: str, index: int, stream, *args) -> None:
@@ -345,6 +354,8 @@ def kq_gemv(fmt: int, x, codes, scales, zeros, tensor_scale, group: int, y,
     if x.dim() != 2 or codes.dim() != 2:
         raise ValueError("x is [m, k] and codes are [n, k/2]")
     (m, k), n, at = x.shape, codes.shape[0], x.get_device()
+    if (k | group) >> 31:
+        _int32(k=k, group=group)
     z = t = None
     if fmt == KQ_FMT_INT4_ASYM:
         s = _want(scales, "scales", torch.float16, (n, k // 128), at)
@@ -366,9 +377,13 @@ class KVCacheInt4:
     """The three arrays of a paged INT4 cache (keys or values) as
     kq_rht_quant_int4_kv writes them: codes uint8 [num_slots, dim/2], scales
     and zeros fp16 [num_slots, dim/128]; with one more leading dimension a
-    cache of several layers.  A view of the caller's tensors, checked once."""
+    cache of several layers.  A view of the caller's tensors, checked
+    once (so they cannot be exchanged)."""
 
-    __slots__ = ("codes", "scales", "zeros", "layers", "num_slots", "dim", "index", "layered")
+    __slots__ = ("_arrays", "layers", "num_slots", "dim", "index", "layered")
+    codes = property(lambda self: self._arrays[0])
+    scales = property(lambda self: self._arrays[1])
+    zeros = property(lambda self: self._arrays[2])
 
     def __init__(self, codes, scales, zeros):
         torch = _torch()
@@ -380,7 +395,7 @@ class KVCacheInt4:
         _want(codes, "codes", torch.uint8, lead + (half,), at)
         _want(scales, "scales", torch.float16, lead + (half // 64,), at)
         _want(zeros, "zeros", torch.float16, lead + (half // 64,), at)
-        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self._arrays = (codes, scales, zeros)
         self.layered = len(lead) == 2
         self.layers = lead[0] if self.layered else 1
         self.num_slots, self.dim, self.index = lead[-1], 2 * half, at
@@ -400,8 +415,12 @@ def kq_attn_decode_int4_kv(q, k_cache: KVCacheInt4, v_cache: KVCacheInt4, k_sign
     int32 [batch]; window > 0 keeps the last `window` tokens and the first
     `sinks` ones visible.  workspace: empty_attn_workspace(...)."""
     torch = _torch()
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q is [batch, q_heads, 128] and block_table [batch, width]")
     batch, q_heads, _ = q.shape
     at, dim, width = q.get_device(), k_cache.dim, block_table.shape[1]
+    if (page_size | window | sinks) >> 31:
+        _int32(page_size=page_size, window=window, sinks=sinks)
     if k_cache.layered or v_cache.layered:
         raise ValueError("the attention reads one layer: pass cache.layer(i)")
     if v_cache.dim != dim or v_cache.num_slots != k_cache.num_slots:
@@ -413,8 +432,7 @@ def kq_attn_decode_int4_kv(q, k_cache: KVCacheInt4, v_cache: KVCacheInt4, k_sign
             _want(q, "q", torch.bfloat16, shape, at), batch, q_heads, dim // 128,
             None if k_signs is None else _want(k_signs, "k_signs", torch.int8, (dim,), at),
             None if v_signs is None else _want(v_signs, "v_signs", torch.int8, (dim,), at),
-            k_cache.codes.data_ptr(), k_cache.scales.data_ptr(), k_cache.zeros.data_ptr(),
-            v_cache.codes.data_ptr(), v_cache.scales.data_ptr(), v_cache.zeros.data_ptr(),
+            *[a.data_ptr() for a in k_cache._arrays], *[a.data_ptr() for a in v_cache._arrays],
             k_cache.num_slots, _want(block_table, "block_table", torch.int32, (batch, width), at),
             width, page_size, _want(seq_lens, "seq_lens", torch.int32, (batch,), at), window,
             sinks, softmax_scale, _want(out, "out", torch.bfloat16, shape, at),
@@ -425,7 +443,11 @@ def kq_kv_copy_pages(pairs, page_size: int, k_cache: KVCacheInt4,
                      v_cache: Optional[KVCacheInt4] = None, stream=None) -> None:
     """Copies pages of the cache(s): pairs int32 [n, 2] of (source, destination)
     page; pairs with a page outside the cache are skipped."""
+    if pairs.dim() != 2:
+        raise ValueError("pairs are [n, 2]")
     at, n = k_cache.index, pairs.shape[0]
+    if page_size >> 31:
+        _int32(page_size=page_size)
     values = (None, None, None)
     if v_cache is not None:
         if v_cache.dim != k_cache.dim or v_cache.num_slots != k_cache.num_slots or \
@@ -433,7 +455,7 @@ def kq_kv_copy_pages(pairs, page_size: int, k_cache: KVCacheInt4,
             raise ValueError("the key and value caches differ in shape")
         if v_cache.index != at:
             raise ValueError(f"the caches are not both on cuda:{at}")
-        values = (v_cache.codes.data_ptr(), v_cache.scales.data_ptr(), v_cache.zeros.data_ptr())
+        values = [a.data_ptr() for a in v_cache._arrays]
     _launch((_lib or lib()).kq_kv_copy_pages, "kq_kv_copy_pages", at, stream,
             _want(pairs, "pairs", _torch().int32, (n, 2), at), n, page_size, k_cache.num_slots,
             k_cache.layers, k_cache.dim, k_cache.codes.data_ptr(), k_cache.scales.data_ptr(),

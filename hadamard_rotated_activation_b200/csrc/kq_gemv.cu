@@ -742,6 +742,7 @@ cudaError_t resident_ctas(int ranks, int* out) {
   int clusters = 0;
   e = cudaOccupancyMaxActiveClusters(&clusters, (const void*)k_gemv<FMT, NT, SMALL>, &cfg);
   if (e != cudaSuccess) return e;
+  if (clusters < 1) return cudaErrorInvalidConfiguration;   // none fits beside what is set aside
   *out = clusters * ranks;
   if (dev < kDevices) known[dev][i].store(*out, std::memory_order_relaxed);
   return cudaSuccess;

@@ -737,3 +737,45 @@ def test_attention_nan_query_stays_in_its_head(batch):
         assert out[b, h].isnan().all()
         out[b, h] = clean[b, h]
     _check_attn(out, q.double().cpu().numpy(), k, v, ks, vs, table, 16, lens, 128 ** -0.5, 0, 0)
+
+
+def test_binding_refuses_sizes_past_32_bits_and_missing_tensors():
+    """Sizes that the C entries' 32 bits would cut are refused, not cut; so are
+    tensors that a format needs and does not get, and other ranks."""
+    q, k, v, ks, vs, table, lens = _case(1, [20, 3], 2, 2, 16)
+    kc, vc, t, n = _upload(k), _upload(v), _dev(table), _dev(lens)
+    ok = dict(q=q, k_cache=kc, v_cache=vc, k_signs=None, v_signs=None, block_table=t, page_size=16,
+              seq_lens=n, softmax_scale=0.1, out=torch.empty_like(q),
+              workspace=kq.empty_attn_workspace(2, 4, 2))
+    for change in (dict(page_size=2 ** 32 + 16), dict(window=2 ** 32 + 5), dict(sinks=2 ** 32),
+                   dict(window=2 ** 31), dict(window=-2 ** 32 + 5), dict(block_table=t[0]),
+                   dict(q=q[0]), dict(seq_lens=None), dict(workspace=ok["workspace"].cpu())):
+        with pytest.raises(ValueError):
+            kq.kq_attn_decode_int4_kv(**{**ok, **change})
+    kq.kq_attn_decode_int4_kv(**{**ok, "window": 2 ** 31 - 1, "sinks": 2 ** 31 - 1})
+    pairs = torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    for args in ((pairs, 2 ** 32 + 16, kc), (pairs[0], 16, kc)):
+        with pytest.raises(ValueError):
+            kq.kq_kv_copy_pages(*args)
+    with pytest.raises(AttributeError):
+        kc.codes = vc.codes[:4]
+    rng = np.random.default_rng(0)
+    x = torch.zeros(2, 256, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(2, 8, device="cuda")
+    for fmt in sorted(FMT):
+        codes, s, z, _ = _weights(rng, fmt, 8, 256)
+        codes, s = _dev(oracle.pack_nibbles(codes)), _dev(s)
+        with pytest.raises(ValueError):
+            kq.kq_gemv(FMT[fmt], x, codes, None, None, None, 128, y)
+        if fmt in ("int4_asym", "nvfp4"):
+            with pytest.raises(ValueError):
+                kq.kq_gemv(FMT[fmt], x, codes, s, None, None, 128, y)
+        else:
+            with pytest.raises(ValueError):
+                kq.kq_gemv(FMT[fmt], x, codes, s, None, None, 2 ** 32 + 128, y)
+    wide = 2 ** 32 + 128
+    with pytest.raises(ValueError):
+        kq.kq_gemv(kq.KQ_FMT_MXFP4, x.new_empty(0, wide),
+                   torch.empty(0, wide // 2, dtype=torch.uint8, device="cuda"),
+                   torch.empty(0, wide // 32, dtype=torch.uint8, device="cuda"), None, None, 128,
+                   y.new_empty(0, 0))
