@@ -33,7 +33,10 @@
 // sequences load the machine alike and nothing depends on host knowledge of
 // the lengths.  A unit that one CTA covers is finished there; the others leave
 // partial sums in the workspace, which a second small kernel (launched as a
-// programmatic dependent) joins in CTA order.
+// programmatic dependent) joins in CTA order.  (Measured instead: a cooperative
+// launch that joins behind a barrier of the grid, 5 us slower in every case; the last
+// CTA of a unit to arrive, 47.6 for 24.5 us.)  Few and short sequences, by what the
+// table and the window allow, are not cut: a CTA takes a unit, and nothing is joined.
 //
 // Per CTA: eight warps compute, each its own head (or its own part of the tokens
 // when there are fewer heads), and fill the shared stages together with 16-byte
@@ -67,6 +70,12 @@ constexpr int kMinTiles = 1;                  // tiles a CTA takes at least
 // What beginning a unit costs, in tiles: the query's rotation and the end of the
 // unit before it.  The tiles are dealt with so many more in front of each unit.
 constexpr int kUnitCost = 2;
+// Where no sequence shows more tokens than this and every unit of one head finds a
+// CTA at once, a CTA takes a unit: no lengths to add up, nothing to join, one launch.
+// 4 sequences, 8 cached and 32 query heads, GPU time (time per call from the host),
+// dealt or alone: 256 tokens 8.0 (12.4) or 7.7 (10.2) us, 512 8.4 (12.4) or 9.6 (11.3),
+// 1024 10.3 (12.4) or 13.2 (14.4); 64 sequences of 128, 512 units, 13.0 or 16.6.
+constexpr int kAloneTokens = 512;
 constexpr int kPartFloats = kCols * 128 + 2 * kCols;   // o, m, l of one head
 
 // Tokens of one sequence: positions v < vis, v + skip from `sinks` on.
@@ -370,7 +379,8 @@ __device__ __forceinline__ void store_result(const AttnArgs& P, float (&v)[16], 
   }
 }
 
-template <int HB>
+// ALONE: a CTA takes one unit, from its first tile to its last.
+template <int HB, bool ALONE>
 __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages) {
   using S = Shape<HB>;
   constexpr int TILE = S::kTile, MB = S::kTok / 16;
@@ -378,12 +388,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
   float* join = reinterpret_cast<float*>(smem + S::kStages * S::kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!ALONE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int most = longest(P);
   const int group = P.q_heads / P.kv_heads, chunks = (group + kCols - 1) / kCols;
   const int blocks = P.kv_heads / HB;
   Walk w;
-  const bool any = begin<TILE>(P, most, blocks, chunks, w);
+  bool any;
+  if constexpr (ALONE) {
+    const int unit = blockIdx.x / chunks;
+    w.chunk = blockIdx.x - unit * chunks;
+    w.b = unit / blocks;
+    w.hb = unit - (int)w.b * blocks;
+    w.seq = sequence(P, most, w.b);
+    w.tile = 0;
+    w.left = w.tiles = (w.seq.vis + TILE - 1) / TILE;
+    any = w.left > 0;
+  } else {
+    any = begin<TILE>(P, most, blocks, chunks, w);
+  }
   // sequences without a visible token have no tile: their rows are zeros
   for (int64_t b = blockIdx.x; b < P.batch; b += gridDim.x)
     if (sequence(P, most, b).vis == 0)
@@ -957,32 +979,50 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_wide(AttnArgs P, int g
   if (warp == 0) store_row(P, red[0], b, qh, kh);
 }
 
-template <int HB>
-cudaError_t launch(const AttnArgs& P, cudaStream_t s) {
+PageDiv page_div(int page_size) {
+  PageDiv d{0, 0};
+  if (page_size > 1) {
+    uint32_t l = 1;
+    while ((1u << l) < (uint32_t)page_size) ++l;
+    d.mul = (uint32_t)(((uint64_t(1) << (31 + l)) + page_size - 1) / page_size);
+    d.shift = l - 1;
+  }
+  return d;
+}
+
+cudaError_t multiprocessors(int* out) {
   // looked up once a device
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices];
-  int dev = 0, sms = 0;
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= kDevices || (sms = known[dev].load(std::memory_order_relaxed)) == 0) {
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (dev >= kDevices || (*out = known[dev].load(std::memory_order_relaxed)) == 0) {
+    e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    if (dev < kDevices) known[dev].store(sms, std::memory_order_relaxed);
+    if (dev < kDevices) known[dev].store(*out, std::memory_order_relaxed);
   }
+  return cudaSuccess;
+}
+
+cudaError_t launch_alone(const AttnArgs& P, int units, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute((const void*)k_attn<1, true>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)Shape<1>::kSmem);
+  if (e != cudaSuccess) return e;
+  k_attn<1, true><<<units, kThreads, Shape<1>::kSmem, s>>>(P, page_div(P.page_size));
+  return cudaGetLastError();
+}
+
+template <int HB>
+cudaError_t launch(const AttnArgs& P, int sms, cudaStream_t s) {
   // (a context's, so set at every call)
-  e = cudaFuncSetAttribute((const void*)k_attn<HB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)Shape<HB>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute((const void*)k_attn<HB, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)Shape<HB>::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-  PageDiv d{0, 0};
-  if (P.page_size > 1) {
-    uint32_t l = 1;
-    while ((1u << l) < (uint32_t)P.page_size) ++l;
-    d.mul = (uint32_t)(((uint64_t(1) << (31 + l)) + P.page_size - 1) / P.page_size);
-    d.shift = l - 1;
-  }
-  k_attn<HB><<<grid, kThreads, Shape<HB>::kSmem, s>>>(P, d);
+  k_attn<HB, false><<<grid, kThreads, Shape<HB>::kSmem, s>>>(P, page_div(P.page_size));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -1023,11 +1063,19 @@ size_t attn_workspace_bytes(int64_t batch, int q_heads, int kv_heads) {
 cudaError_t launch_attn_decode(const AttnArgs& args, cudaStream_t s) {
   AttnArgs P = args;
   if (P.num_slots == 0) P.table_width = 0;    // no row to read: every sequence is empty
+  int sms = 0;
+  const cudaError_t e = at::multiprocessors(&sms);
+  if (e != cudaSuccess) return e;
+  const int chunks = (P.q_heads / P.kv_heads + at::kCols - 1) / at::kCols;
+  const int64_t units = P.batch * P.kv_heads * chunks, keep = (int64_t)P.window + P.sinks;
+  const int64_t longest = P.table_width * P.page_size;
+  if (units <= 2 * sms && (P.window > 0 && keep < longest ? keep : longest) <= at::kAloneTokens)
+    return at::launch_alone(P, (int)units, s);
   // the widest block of heads whose rows and scales stay whole
-  if (P.kv_heads % 8 == 0) return at::launch<8>(P, s);
-  if (P.kv_heads % 4 == 0) return at::launch<4>(P, s);
-  if (P.kv_heads % 2 == 0) return at::launch<2>(P, s);
-  return at::launch<1>(P, s);
+  if (P.kv_heads % 8 == 0) return at::launch<8>(P, sms, s);
+  if (P.kv_heads % 4 == 0) return at::launch<4>(P, sms, s);
+  if (P.kv_heads % 2 == 0) return at::launch<2>(P, sms, s);
+  return at::launch<1>(P, sms, s);
 }
 
 }  // namespace kq

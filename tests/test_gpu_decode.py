@@ -779,3 +779,45 @@ def test_binding_refuses_sizes_past_32_bits_and_missing_tensors():
                    torch.empty(0, wide // 2, dtype=torch.uint8, device="cuda"),
                    torch.empty(0, wide // 32, dtype=torch.uint8, device="cuda"), None, None, 128,
                    y.new_empty(0, 0))
+
+
+# Short tables take the units of a batch one by one; the sizes above once more behind
+# tables wide enough (more than 512 tokens) that the same lengths are dealt and joined.
+def _dealt(page):
+    return dict(extra_width=512 // page + 1)
+
+
+@pytest.mark.parametrize("heads,group", [(1, 1), (1, 8), (2, 3), (3, 2), (4, 4), (5, 5), (6, 1),
+                                         (8, 1), (8, 4), (8, 8), (12, 2), (16, 2), (2, 16), (1, 20),
+                                         (32, 1)])
+def test_attention_head_layouts_dealt(heads, group):
+    _whole(heads * 100 + group, [1, 33, 150, 0, 17], heads, group, 16, **_dealt(16))
+
+
+@pytest.mark.parametrize("page", [1, 3, 7, 16, 24, 32, 50, 64, 128])
+def test_attention_pages_dealt(page):
+    _whole(page, [200, 1, 31, 32, 33, 129, 63, 64, 65], 8, 2, page, **_dealt(page))
+
+
+@pytest.mark.parametrize("lens", [[1], [2], [15], [16], [17], [31], [32], [33], [127], [128],
+                                  [129], [255], [256], [257], [0], [0, 0, 3]])
+def test_attention_lengths_dealt(lens):
+    _whole(sum(lens), lens, 2, 4, 16, **_dealt(16))
+    _whole(sum(lens) + 1, lens, 8, 4, 16, **_dealt(16))
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 3), (64, 0), (100, 1), (256, 256), (256, 257),
+                                          (512, 0), (2 ** 31 - 1, 2 ** 31 - 1)])
+@pytest.mark.parametrize("heads,group", [(8, 4), (2, 9)])
+def test_attention_windows_on_long_tables(heads, group, window, sinks):
+    """A window of few tokens on a long table is short too; on either side of 512."""
+    _whole(window + sinks, [1, 5, 40, 600, 2000, 0, 333, 513], heads, group, 16, window, sinks)
+
+
+@pytest.mark.parametrize("batch", [18, 19, 36, 37, 38, 74, 75])
+def test_attention_short_units_around_the_ctas(batch):
+    """Numbers of (sequence, head) units around one and two CTAs a multiprocessor."""
+    rng = np.random.default_rng(batch)
+    lens = [int(n) for n in rng.integers(0, 513, batch)]
+    for heads, group in ((8, 2), (4, 9)):
+        _whole(batch, lens, heads, group, 32, **(dict(extra_width=16 - max(-(-n // 32) for n in lens))))
