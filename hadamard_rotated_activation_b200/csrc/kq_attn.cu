@@ -21,9 +21,9 @@
 // heads that share the cached head, and at the memory's rate it needs 3/8 of
 // that path's throughput; the accumulators stay where the softmax is computed.
 // Measured (one B200, time between calls in a graph): one sequence of 131071
-// tokens, 8 cached and 64 query heads, 42.8 us = 3.3 TB/s, of which 30 us are the
+// tokens, 8 cached and 64 query heads, 42.1 us = 3.4 TB/s, of which 30 us are the
 // tiles, 6 the start (lengths, pages and query, one memory latency behind the other)
-// and 6 the join; 32 sequences of 300 to 4096 tokens 24.4 us.  In the tiles memory and
+// and 5 the join; 32 sequences of 300 to 4096 tokens 22.8 us.  In the tiles memory and
 // instruction issue are near each other: without the copies they take 25 us, at 1.9
 // to 2.0 instructions a cycle, half of them on the integer pipe (unpacking).
 //
@@ -802,10 +802,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 to[i] = make_float4(r[j][4 * i], r[j][4 * i + 1], r[j][4 * i + 2], r[j][4 * i + 3]);
-              if (g == 0) {
-                slot[kCols * 128 + 2 * t + j] = m[j];
-                slot[kCols * 128 + kCols + 2 * t + j] = l[j];
-              }
+              if (g == 0)
+                reinterpret_cast<float2*>(slot + kCols * 128)[2 * t + j] = make_float2(m[j], l[j]);
             }
         }
       }
@@ -857,6 +855,8 @@ __device__ __forceinline__ Parts parts_of(const AttnArgs& P, int grid, int64_t b
 
 // Maximum, sum and values (4 dimensions a lane) of column `col` over the partial
 // sums i0, i0 + by, ...; AHEAD of them are loaded at a time, with a running maximum.
+// (A CTA a row: 10, 131071 tokens 42.0 us and 42.7 with 4; a warp a row: 6, 64 windows of
+// 1028 tokens 27.4 us and 27.8 with 8 or 10.)
 struct Joined {
   float m, l;
   float4 v;
@@ -876,8 +876,9 @@ __device__ __forceinline__ Joined sum_parts(const Parts& p, int col, int i0, int
       v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (i < p.n) {
         const float* s = p.slot(i);
-        pm[k] = s[kCols * 128 + col];
-        pl[k] = s[kCols * 128 + kCols + col];
+        const float2 ml = reinterpret_cast<const float2*>(s + kCols * 128)[col];
+        pm[k] = ml.x;
+        pl[k] = ml.y;
         v[k] = *reinterpret_cast<const float4*>(s + col * 128 + 4 * lane);
       }
     }
@@ -903,80 +904,89 @@ __device__ __forceinline__ Joined sum_parts(const Parts& p, int col, int i0, int
   }
   return r;
 }
-// A warp stores the row whose 128 values lie in shared memory.
-__device__ __forceinline__ void store_row(const AttnArgs& P, const float* row, int64_t b, int qh,
-                                          int kh) {
-  const int lane = threadIdx.x & 31, g = lane >> 2;
-  float v[16];
+// Signs of a lane's 4 dimensions of a cached head.
+__device__ __forceinline__ uint32_t join_signs(const AttnArgs& P, int kh) {
+  const int at = kh * 128 + 4 * (threadIdx.x & 31);
+  return P.v_signs ? __ldg(reinterpret_cast<const uint32_t*>(P.v_signs + at)) : 0;
+}
+// A warp rotates a joined row back, 4 dimensions a lane, and stores it.
+__device__ __forceinline__ void store_joined(const AttnArgs& P, float l, float4 v, uint32_t signs,
+                                             int64_t b, int qh) {
+  const int lane = threadIdx.x & 31;
+  const float inv = l == 0.0f ? 0.0f : 0.08838834764831845f / l;
+  float r[4] = {v.x + v.y, v.x - v.y, v.z + v.w, v.z - v.w};
+  const float a0 = r[0], a1 = r[1];
+  r[0] = (a0 + r[2]) * inv;
+  r[1] = (a1 + r[3]) * inv;
+  r[2] = (a0 - r[2]) * inv;
+  r[3] = (a1 - r[3]) * inv;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 f = *reinterpret_cast<const float4*>(row + 16 * g + 4 * i);
-    v[4 * i] = f.x;
-    v[4 * i + 1] = f.y;
-    v[4 * i + 2] = f.z;
-    v[4 * i + 3] = f.w;
+  for (int st = 1; st < 32; st <<= 1) {
+    const float own = (lane & st) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = fmaf(own, r[i], __shfl_xor_sync(0xffffffffu, r[i], st));
   }
-  store_result(P, v, b, qh, kh, (lane & 3) == 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = __uint_as_float(__float_as_uint(r[i]) ^ (signs << (24 - 8 * i) & 0x80000000u));
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(r[0], r[1]), hi = __floats2bfloat162_rn(r[2], r[3]);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + (b * P.q_heads + qh) * 128 + 4 * lane) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 // Many rows: a CTA takes (sequence, cached head, chunk of its query heads), a warp
 // a query head at a time.
 template <int HB>
 __global__ void __launch_bounds__(32 * kRowWarps) k_join_rows(AttnArgs P, int grid) {
-  __shared__ __align__(16) float rows[kRowWarps][128];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int group = P.q_heads / P.kv_heads, chunks = (group + kCols - 1) / kCols;
   const int64_t b = blockIdx.x;
   const int kh = blockIdx.y / chunks, chunk = blockIdx.y - kh * chunks;
   const Parts p = parts_of<HB>(P, grid, b, kh, chunk);
+  const uint32_t signs = join_signs(P, kh);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p.n < 2) return;
   const int columns = min(kCols, group - chunk * kCols);
   for (int col = warp; col < columns; col += kRowWarps) {
-    const Joined r = sum_parts<8>(p, col, 0, 1);
-    const float inv = r.l > 0.0f ? 1.0f / r.l : 0.0f;
-    __syncwarp();
-    *reinterpret_cast<float4*>(&rows[warp][4 * lane]) =
-        make_float4(r.v.x * inv, r.v.y * inv, r.v.z * inv, r.v.w * inv);
-    __syncwarp();
-    store_row(P, rows[warp], b, kh * group + chunk * kCols + col, kh);
+    const Joined r = sum_parts<6>(p, col, 0, 1);
+    store_joined(P, r.l, r.v, signs, b, kh * group + chunk * kCols + col);
   }
 }
 
 // Fewer rows, which may have partial sums of many CTAs: a CTA takes one.
 template <int HB, int kJoinWarps>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join_wide(AttnArgs P, int grid) {
-  __shared__ float wm[kJoinWarps], wl[kJoinWarps];
+  __shared__ float2 ml[kJoinWarps];
   __shared__ __align__(16) float red[kJoinWarps][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t b = blockIdx.x;
   const int qh = blockIdx.y, group = P.q_heads / P.kv_heads, kh = qh / group;
   const int chunk = (qh - kh * group) / kCols, col = (qh - kh * group) % kCols;
   const Parts p = parts_of<HB>(P, grid, b, kh, chunk);
+  const uint32_t signs = warp == 0 ? join_signs(P, kh) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p.n < 2) return;
-  const Joined r = sum_parts<4>(p, col, warp, kJoinWarps);
+  const Joined r = sum_parts<10>(p, col, warp, kJoinWarps);
   *reinterpret_cast<float4*>(&red[warp][4 * lane]) = r.v;
-  if (lane == 0) {
-    wm[warp] = r.m;
-    wl[warp] = r.l;
-  }
+  if (lane == 0) ml[warp] = make_float2(r.m, r.l);
   __syncthreads();
-  if (threadIdx.x < 128) {
-    float top = -INFINITY, sum = 0.0f, ls = 0.0f;
+  if (warp > 0) return;
+  float top = -INFINITY, ls = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, wm[k]);
-    const float ref = top == -INFINITY ? 0.0f : top;
+  for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, ml[k].x);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) {
-      const float f = exp2_(wm[k] - ref);
-      sum = fmaf(f, red[k][threadIdx.x], sum);
-      ls = fmaf(f, wl[k], ls);
-    }
-    red[0][threadIdx.x] = ls == 0.0f ? 0.0f : sum / ls;
+  for (int k = 0; k < kJoinWarps; ++k) {
+    const float f = exp2_(ml[k].x - ref);
+    const float4 o = *reinterpret_cast<const float4*>(&red[k][4 * lane]);
+    ls = fmaf(f, ml[k].y, ls);
+    v.x = fmaf(f, o.x, v.x);
+    v.y = fmaf(f, o.y, v.y);
+    v.z = fmaf(f, o.z, v.z);
+    v.w = fmaf(f, o.w, v.w);
   }
-  __syncthreads();
-  if (warp == 0) store_row(P, red[0], b, qh, kh);
+  store_joined(P, ls, v, signs, b, qh);
 }
 
 PageDiv page_div(int page_size) {
@@ -1034,7 +1044,7 @@ cudaError_t launch(const AttnArgs& P, int sms, cudaStream_t s) {
   cfg.numAttrs = 1;
   // A row's CTA of 16 warps, 4 or 1, as far as they all run at a time: 32
   // sequences of 32 heads (1024 rows) took 24.4 us with 4 warps and 25.5 with 1,
-  // 2048 rows 31.0 with 4 and 28.1 with 1.
+  // 2048 rows 31.0 with 4 and 28.1 with 1 (before the join held 4 dimensions a lane).
   const int64_t rows = P.batch * P.q_heads;
   cfg.gridDim = dim3((unsigned)P.batch, (unsigned)P.q_heads);
   if (rows <= 2 * sms) {
