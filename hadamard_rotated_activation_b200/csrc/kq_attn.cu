@@ -83,7 +83,7 @@ struct Seq {
   int vis, skip;
 };
 __device__ __forceinline__ Seq sequence(const AttnArgs& P, int most, int64_t b) {
-  const int len = min(max(__ldg(P.seq_lens + b), 0), most);
+  const int len = min(max(P.seq_lens[b], 0), most);
   const int64_t keep = (int64_t)P.window + P.sinks;
   Seq s;
   s.skip = P.window > 0 && len > keep ? (int)(len - keep) : 0;
@@ -233,7 +233,7 @@ __device__ __forceinline__ Place place(const AttnArgs& P, PageDiv d, const Walk&
   if (v >= w.seq.vis) return Place{-1, 0};
   const uint32_t pos = (uint32_t)(v < P.sinks ? v : v + w.seq.skip);
   const uint32_t page_in = page_of(d, pos);
-  return Place{__ldg(P.block_table + w.b * P.table_width + page_in),
+  return Place{P.block_table[w.b * P.table_width + page_in],
                (int)(pos - page_in * (uint32_t)P.page_size)};
 }
 // Its cache row, -1 where there is none.
@@ -357,7 +357,7 @@ __device__ __forceinline__ void store_result(const AttnArgs& P, float (&v)[16], 
   const int d0 = 16 * ((threadIdx.x & 31) >> 2);
   uint32_t w[8];
   uint4 sg = make_uint4(0, 0, 0, 0);
-  if (P.v_signs) sg = __ldg(reinterpret_cast<const uint4*>(P.v_signs + kh * 128 + d0));
+  if (P.v_signs) sg = *reinterpret_cast<const uint4*>(P.v_signs + kh * 128 + d0);
   const uint32_t s4[4] = {sg.x, sg.y, sg.z, sg.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -388,6 +388,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
   float* join = reinterpret_cast<float*>(smem + S::kStages * S::kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the join, which reads the lengths ahead of its own wait: behind this one
   if (!ALONE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int most = longest(P);
   const int group = P.q_heads / P.kv_heads, chunks = (group + kCols - 1) / kCols;
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
         copy_lines<HB>(to, P.k_codes + off);
         copy_lines<HB>(to + S::kCodes, P.v_codes + off);
         if constexpr (HB == 1) {
-          sreg[j] = r >= 0 ? __ldg(sc_from + row) : 0;
+          sreg[j] = r >= 0 ? sc_from[row] : 0;
         } else {
           if (arr < 4)
             copy_or_zero<2 * HB>(my_scales + base + j * S::kPass * HB * 2, sc_from + row, r >= 0);
@@ -510,10 +512,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
           const uint4* sp = reinterpret_cast<const uint4*>(P.k_signs + kh * 128 + 32 * t);
           uint4 v[4], sg[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = __ldg(from + i);
+          for (int i = 0; i < 4; ++i) v[i] = from[i];
           if (P.k_signs) {
-            sg[0] = __ldg(sp);
-            sg[1] = __ldg(sp + 1);
+            sg[0] = sp[0];
+            sg[1] = sp[1];
           }
           const uint32_t ok = g < columns ? 0xffffffffu : 0u;
 #pragma unroll
@@ -907,7 +909,7 @@ __device__ __forceinline__ Joined sum_parts(const Parts& p, int col, int i0, int
 // Signs of a lane's 4 dimensions of a cached head.
 __device__ __forceinline__ uint32_t join_signs(const AttnArgs& P, int kh) {
   const int at = kh * 128 + 4 * (threadIdx.x & 31);
-  return P.v_signs ? __ldg(reinterpret_cast<const uint32_t*>(P.v_signs + at)) : 0;
+  return P.v_signs ? *reinterpret_cast<const uint32_t*>(P.v_signs + at) : 0;
 }
 // A warp rotates a joined row back, 4 dimensions a lane, and stores it.
 __device__ __forceinline__ void store_joined(const AttnArgs& P, float l, float4 v, uint32_t signs,
@@ -1020,8 +1022,10 @@ cudaError_t launch_alone(const AttnArgs& P, int units, cudaStream_t s) {
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)Shape<1>::kSmem);
   if (e != cudaSuccess) return e;
-  k_attn<1, true><<<units, kThreads, Shape<1>::kSmem, s>>>(P, page_div(P.page_size));
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      dependent_launch(dim3((unsigned)units), kThreads, Shape<1>::kSmem, s, attr);
+  return cudaLaunchKernelEx(&cfg, k_attn<1, true>, P, page_div(P.page_size));
 }
 
 template <int HB>
@@ -1032,32 +1036,25 @@ cudaError_t launch(const AttnArgs& P, int sms, cudaStream_t s) {
                                        (int)Shape<HB>::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-  k_attn<HB, false><<<grid, kThreads, Shape<HB>::kSmem, s>>>(P, page_div(P.page_size));
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cudaLaunchConfig_t cfg =
+      dependent_launch(dim3((unsigned)grid), kThreads, Shape<HB>::kSmem, s, attr);
+  e = cudaLaunchKernelEx(&cfg, k_attn<HB, false>, P, page_div(P.page_size));
+  if (e != cudaSuccess) return e;
   // A row's CTA of 16 warps, 4 or 1, as far as they all run at a time: 32
   // sequences of 32 heads (1024 rows) took 24.4 us with 4 warps and 25.5 with 1,
   // 2048 rows 31.0 with 4 and 28.1 with 1 (before the join held 4 dimensions a lane).
   const int64_t rows = P.batch * P.q_heads;
-  cfg.gridDim = dim3((unsigned)P.batch, (unsigned)P.q_heads);
-  if (rows <= 2 * sms) {
-    cfg.blockDim = dim3(32 * 16);
-    return cudaLaunchKernelEx(&cfg, k_join_wide<HB, 16>, P, grid);
-  }
   if (rows <= 8 * sms) {
-    cfg.blockDim = dim3(32 * 4);
-    return cudaLaunchKernelEx(&cfg, k_join_wide<HB, 4>, P, grid);
+    const dim3 each((unsigned)P.batch, (unsigned)P.q_heads);
+    const bool few = rows <= 2 * sms;
+    cfg = dependent_launch(each, few ? 32 * 16 : 32 * 4, 0, s, attr);
+    return few ? cudaLaunchKernelEx(&cfg, k_join_wide<HB, 16>, P, grid)
+               : cudaLaunchKernelEx(&cfg, k_join_wide<HB, 4>, P, grid);
   }
   const int chunks = (P.q_heads / P.kv_heads + kCols - 1) / kCols;
-  cfg.gridDim = dim3((unsigned)P.batch, (unsigned)(P.kv_heads * chunks));
-  cfg.blockDim = dim3(32 * kRowWarps);
+  cfg = dependent_launch(dim3((unsigned)P.batch, (unsigned)(P.kv_heads * chunks)),
+                         32 * kRowWarps, 0, s, attr);
   return cudaLaunchKernelEx(&cfg, k_join_rows<HB>, P, grid);
 }
 

@@ -167,8 +167,8 @@ __device__ __forceinline__ Eight load8(const Params& P, int tok, int k0) {
     const int64_t at = (int64_t)tok * P.k + k0;
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(P.x) +
                                                     at * (P.x_bf16 ? 2 : 4));
-    e.a = __ldg(p);
-    if (!P.x_bf16) e.b = __ldg(p + 1);
+    e.a = p[0];
+    if (!P.x_bf16) e.b = p[1];
   }
   return e;
 }
@@ -347,20 +347,37 @@ struct Stream {
       return;
     }
     // scales that no aligned copy reaches: one by one
-    const int per = FMT == KQ_FMT_INT4_ASYM ? 1 : FMT == KQ_FMT_NVFP4 ? 8 : 4;   // a group
+    constexpr int per = FMT == KQ_FMT_INT4_ASYM ? 1 : FMT == KQ_FMT_NVFP4 ? 8 : 4;   // a group
+    constexpr int kTurns = 16 * kStep * per / 32, kAhead = kTurns < 8 ? kTurns : 8;
     const int count = FMT == KQ_FMT_INT4_ASYM ? P.groups : FMT == KQ_FMT_NVFP4 ? P.k / 16 : P.k / 32;
     const int left = (int)min(P.n - 1 - row0, (int64_t)15);
-    for (int i = lane; i < 16 * kStep * per; i += 32) {
-      const int row = i / (kStep * per), e = i - row * (kStep * per), at = g0 * per + e;
-      const int64_t src = (row0 + min(left, row)) * count + at;
-      const bool ok = at < gend * per && at < count;
-      uint8_t* d = stage + 16 * S::kRow + row * S::kScaleRow;
-      if (FMT == KQ_FMT_INT4_ASYM) {
-        reinterpret_cast<uint16_t*>(d)[e] =
-            ok ? __ldg(static_cast<const uint16_t*>(P.scales) + src) : 0;
-        reinterpret_cast<uint16_t*>(d)[kStep + e] = ok ? __ldg(P.zeros + src) : 0;
-      } else {
-        d[e] = ok ? __ldg(static_cast<const uint8_t*>(P.scales) + src) : 0;
+#pragma unroll 1
+    for (int j0 = 0; j0 < kTurns; j0 += kAhead) {
+      uint16_t v[kAhead], z[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = lane + 32 * (j0 + j), row = i / (kStep * per), e = i - row * (kStep * per);
+        const int at = g0 * per + e;
+        const int64_t src = (row0 + min(left, row)) * count + at;
+        const bool ok = at < gend * per && at < count;
+        v[j] = z[j] = 0;
+        if (FMT == KQ_FMT_INT4_ASYM) {
+          if (ok) v[j] = static_cast<const uint16_t*>(P.scales)[src];
+          if (ok) z[j] = P.zeros[src];
+        } else if (ok) {
+          v[j] = static_cast<const uint8_t*>(P.scales)[src];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = lane + 32 * (j0 + j), row = i / (kStep * per), e = i - row * (kStep * per);
+        uint8_t* d = stage + 16 * S::kRow + row * S::kScaleRow;
+        if (FMT == KQ_FMT_INT4_ASYM) {
+          reinterpret_cast<uint16_t*>(d)[e] = v[j];
+          reinterpret_cast<uint16_t*>(d)[kStep + e] = z[j];
+        } else {
+          d[e] = (uint8_t)v[j];
+        }
       }
     }
   }
@@ -548,6 +565,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   constexpr bool SUMS = FMT == KQ_FMT_INT4_ASYM || (FMT == KQ_FMT_INT4_SYM && SMALL);
   constexpr int kWarps = S::kWarps, kStep = S::kStep, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
+  // (what lies behind it is read by plain loads: a read-only load has no order with it)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int ranks = P.ranks, rank = ranks > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * (kStages * S::kStage);
@@ -674,7 +693,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
     // a lane a row
     const int mine = (tiles - rank + ranks - 1) >> P.rank_shift;    // tiles this CTA owns
     const int pairs = (mt + 1) >> 1, slots = ranks * parts, pitch = own * 16 * mt;
-    const float t_scale = FMT == KQ_FMT_NVFP4 ? __ldg(P.tscale) : 1.0f;
+    const float t_scale = FMT == KQ_FMT_NVFP4 ? *P.tscale : 1.0f;
     for (int q = warp; q < mine * pairs; q += kWarps) {
       const int tl = q / pairs, tok = 2 * (q - tl * pairs) + (lane >> 4), r = lane & 15;
       const int64_t row = row0 + ((tl << P.rank_shift) + rank) * 16 + r;
@@ -684,7 +703,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
 #pragma unroll 8
       for (int c = 0; c < slots; ++c) v += from[c * pitch];
       if (SMALL) v *= 0x1p24f;              // the codes' 2^-24
-      if (FMT == KQ_FMT_INT4_SYM) v *= __ldg(static_cast<const float*>(P.scales) + row);
+      if (FMT == KQ_FMT_INT4_SYM) v *= static_cast<const float*>(P.scales)[row];
       if (FMT == KQ_FMT_NVFP4) v *= t_scale;
       const int64_t at = tok * P.n + row;
       if (P.y_bf16)
@@ -799,17 +818,13 @@ cudaError_t launch(Params P, cudaStream_t s) {
   e = cudaFuncSetAttribute((const void*)k_gemv<FMT, NT, SMALL>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, R::kAll);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((all + P.tiles - 1) / P.tiles * ranks));
-  cfg.blockDim = dim3(Shape<NT>::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ranks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = ranks > 1 ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  const cudaLaunchConfig_t cfg =
+      dependent_launch(dim3((unsigned)((all + P.tiles - 1) / P.tiles * ranks)),
+                       Shape<NT>::kThreads, smem, s, attr, ranks > 1 ? 1 : 0);
   return cudaLaunchKernelEx(&cfg, k_gemv<FMT, NT, SMALL>, P);
 }
 

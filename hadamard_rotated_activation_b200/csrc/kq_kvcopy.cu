@@ -8,8 +8,9 @@
 // pieces a thread of the key and of the value codes, and in the first slice the
 // short scale and zero-point pages (two bytes a token and head, in the widest unit
 // that divides both a page's and a layer's bytes) -- are on their way before the
-// first store: 1500 pages of 16 tokens and 8 heads in 4 layers take 35.6 us (5.9
-// TB/s, 0.90 of the copy rate), and took 56.6 with one array after the other.
+// first store: 1500 pages of 16 tokens and 8 heads in 4 layers take 34.4 us (6.1
+// TB/s, 0.93 of the copy rate; 35.4 with loads marked as read once), and took 56.6 with
+// one array after the other.
 #include <cstdint>
 
 #include "kq_internal.h"
@@ -44,9 +45,13 @@ __device__ __forceinline__ void copy_slice(const Params& P, int64_t src, int64_t
   const int64_t all = blockIdx.y == 0 ? each * 2 * P.arrays : 0;
   int64_t i = threadIdx.x;
   auto small_at = [&](int64_t base, int64_t at) {
-    const int a = (int)((uint64_t)at >= (uint64_t)(2 * each)) * 2;
-    const int b = a + (int)(at - a * each >= each);
-    return reinterpret_cast<T*>(reinterpret_cast<char*>(P.small_[b]) + base) + (at - b * each);
+    const bool vals = at >= 2 * each;
+    at -= vals ? 2 * each : 0;
+    const bool zero = at >= each;
+    at -= zero ? each : 0;
+    uint16_t* const sp = vals ? P.small_[2] : P.small_[0];
+    uint16_t* const zp = vals ? P.small_[3] : P.small_[1];
+    return reinterpret_cast<T*>(reinterpret_cast<char*>(zero ? zp : sp) + base) + at;
   };
   do {
     uint4 k[kUnroll], v[kUnroll];
@@ -54,9 +59,9 @@ __device__ __forceinline__ void copy_slice(const Params& P, int64_t src, int64_t
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j)
       if (u + j * kThreads < units) {
-        k[j] = __ldcs(reinterpret_cast<const uint4*>(P.codes[0] + src) + u + j * kThreads);
+        k[j] = __ldcg(reinterpret_cast<const uint4*>(P.codes[0] + src) + u + j * kThreads);
         if (P.arrays > 1)
-          v[j] = __ldcs(reinterpret_cast<const uint4*>(P.codes[1] + src) + u + j * kThreads);
+          v[j] = __ldcg(reinterpret_cast<const uint4*>(P.codes[1] + src) + u + j * kThreads);
       }
     if (i < all) t = *small_at(ssrc, i);
 #pragma unroll
@@ -72,9 +77,15 @@ __device__ __forceinline__ void copy_slice(const Params& P, int64_t src, int64_t
 }
 
 __global__ void __launch_bounds__(kThreads) k_copy_pages(Params P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t layer = blockIdx.x / (uint32_t)P.n_pairs;
   const uint32_t pair = blockIdx.x - layer * (uint32_t)P.n_pairs;
-  const int2 sd = __ldg(reinterpret_cast<const int2*>(P.pairs) + pair);
+  // in order with the wait; the pages' loads follow from it
+  int2 sd;
+  asm volatile("ld.global.v2.s32 {%0, %1}, [%2];"
+               : "=r"(sd.x), "=r"(sd.y)
+               : "l"(P.pairs + 2 * (int64_t)pair)
+               : "memory");
   const int64_t s = sd.x, d = sd.y;
   if (s < 0 || d < 0 || s >= P.pages || d >= P.pages || s == d) return;
   const int64_t src = layer * P.code_layer + s * P.code_page;
@@ -110,9 +121,10 @@ cudaError_t launch_kv_copy(const int32_t* pairs, int64_t n_pairs, int page_size,
   const int64_t slice = 16 * kvc::kThreads * kvc::kUnroll;
   int64_t slices = (P.code_page + slice - 1) / slice;
   if (slices > 1024) slices = 1024;
-  kvc::k_copy_pages<<<dim3((unsigned)(n_pairs * layers), (unsigned)slices), kvc::kThreads, 0,
-                      s>>>(P);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = dependent_launch(
+      dim3((unsigned)(n_pairs * layers), (unsigned)slices), kvc::kThreads, 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, kvc::k_copy_pages, P);
 }
 
 }  // namespace kq

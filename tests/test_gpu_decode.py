@@ -821,3 +821,134 @@ def test_attention_short_units_around_the_ctas(batch):
     lens = [int(n) for n in rng.integers(0, 513, batch)]
     for heads, group in ((8, 2), (4, 9)):
         _whole(batch, lens, heads, group, 32, **(dict(extra_width=16 - max(-(-n // 32) for n in lens))))
+
+
+# ----------------------------------- calls right behind what makes their inputs
+def test_decode_calls_right_behind_their_inputs():
+    """The kernels may be brought in while the one in front of them ends: inputs
+    written by it (kernels, copies and sets, on the same or another stream, in
+    captured graphs too) are the ones that are read, and what comes behind a call
+    sees its result."""
+    rng = np.random.default_rng(8)
+    heads, group, page = 8, 4, 16
+    q, k, v, ks, vs, table, lens = _case(41, [900, 70, 1300, 5], heads, group, page)
+    kc, vc, ksd, vsd = _upload(k), _upload(v), _dev(ks), _dev(vs)
+    w = _weights(rng, "int4_asym", 500, 2048)
+    codes, sc, z = _dev(oracle.pack_nibbles(w[0])), _dev(w[1]), _dev(w[2])
+    # two sets of inputs, and results of calls that had all the time they want
+    qs = [q, q.flip(0).contiguous()]
+    ls = [_dev(lens), _dev(lens // 2)]
+    xs = [torch.from_numpy(rng.standard_normal((3, 2048))).cuda().bfloat16() for _ in range(2)]
+    tab, ws = _dev(table), kq.empty_attn_workspace(4, heads * group, heads)
+    want = []
+    for i in range(2):
+        y = torch.empty(3, 500, device="cuda")
+        kq.kq_gemv(kq.KQ_FMT_INT4_ASYM, xs[i], codes, sc, z, None, 128, y)
+        torch.cuda.synchronize()
+        want.append((_attn(qs[i], kc, vc, ksd, vsd, tab, page, ls[i], 0.1), y))
+        torch.cuda.synchronize()
+    which = torch.zeros((), dtype=torch.int64, device="cuda")
+    qb, lb, xb = torch.empty_like(q), torch.empty_like(ls[0]), torch.empty_like(xs[0])
+    out, yb = torch.empty_like(q), torch.empty(3, 500, device="cuda")
+    res, yres = torch.empty_like(out), torch.empty_like(yb)
+    allq, alll, allx = torch.stack(qs), torch.stack(ls), torch.stack(xs)
+    busy = torch.zeros(1 << 24, device="cuda")
+    other = torch.cuda.Stream()
+    pinned = [n.cpu().pin_memory() for n in ls]
+
+    def kernels(i):
+        busy.add_(1.0)                       # keeps the multiprocessors while the call is issued
+        torch.index_select(allq, 0, which.view(1), out=qb.unsqueeze(0))
+        torch.index_select(alll, 0, which.view(1), out=lb.unsqueeze(0))
+
+    def copies(i):
+        qb.copy_(qs[i])
+        lb.copy_(pinned[i], non_blocking=True)
+
+    def across(i):
+        main = torch.cuda.current_stream()
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            kernels(i)
+        busy.mul_(0.5)
+        main.wait_stream(other)
+
+    def step(i, before):
+        before(i)
+        kq.kq_attn_decode_int4_kv(qb, kc, vc, ksd, vsd, tab, page, lb, 0.1, out, ws)
+        res.copy_(out)
+        torch.index_select(allx, 0, which.view(1), out=xb.unsqueeze(0))
+        yb.zero_()
+        kq.kq_gemv(kq.KQ_FMT_INT4_ASYM, xb, codes, sc, z, None, 128, yb)
+        yres.copy_(yb)
+
+    def check(i):
+        torch.cuda.synchronize()
+        assert torch.equal(res, want[i][0]) and torch.equal(yres, want[i][1])
+    for before in (kernels, copies, across):
+        for turn in range(12):
+            which.fill_(turn & 1)
+            for a in (qb, out, res):
+                a.fill_(float("nan"))
+            step(turn & 1, before)
+            check(turn & 1)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graphs = []
+        for i in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                step(i, before)
+            graphs.append(g)
+        for turn in range(12):
+            which.fill_(turn & 1)
+            for a in (qb, out, res, yb, yres):
+                a.fill_(float("nan"))
+            graphs[turn & 1].replay()
+            check(turn & 1)
+
+
+def test_decode_calls_in_a_chain():
+    """Page copies, attention and products one behind the other with nothing in
+    between, each reading what the one in front wrote, against the same calls with a
+    synchronization behind each."""
+    heads, group, page = 8, 2, 16
+    q, k, v, ks, vs, table, lens = _case(43, [333, 48, 700], heads, group, page, spare=12)
+    rng = np.random.default_rng(9)
+    n = heads * group * 128
+    w = [_weights(rng, f, n, n) for f in ("int4_asym", "mxfp4")]
+    w = [(_dev(oracle.pack_nibbles(c)), _dev(s * 0.02 if i == 0 else s),
+          None if zz is None else _dev(zz)) for i, (c, s, zz, _) in enumerate(w)]
+    pages = k[0].shape[0] // page
+    spare = [p for p in range(pages) if p not in set(table.ravel().tolist())]
+    pairs = _dev(np.array([[table[0, 0], spare[0]], [table[1, 1], spare[1]]], dtype=np.int32))
+    table2 = table.copy()
+    table2[0, 0], table2[1, 1] = spare[0], spare[1]
+    tab, ln, ws = _dev(table2), _dev(lens), kq.empty_attn_workspace(3, heads * group, heads)
+
+    def run(wait):
+        def then():
+            if wait:
+                torch.cuda.synchronize()
+        kc, vc = _upload(k), _upload(v)
+        torch.cuda.synchronize()
+        x, results = q.clone(), []
+        for turn in range(4):
+            kq.kq_kv_copy_pages(pairs, page, kc, vc)
+            then()
+            out = torch.empty_like(q)
+            kq.kq_attn_decode_int4_kv(x, kc, vc, None, None, tab, page, ln, 0.02, out, ws)
+            then()
+            y = torch.empty(3, n, dtype=torch.bfloat16, device="cuda")
+            kq.kq_gemv(kq.KQ_FMT_INT4_ASYM, out.view(3, n), *w[0], None, 128, y)
+            then()
+            y2 = torch.empty(3, n, dtype=torch.bfloat16, device="cuda")
+            kq.kq_gemv(kq.KQ_FMT_MXFP4, y, w[1][0], w[1][1], None, None, 128, y2)
+            then()
+            x = (y2 / 64).clamp(-4, 4).view_as(q)
+            results += [out, y, y2]
+        torch.cuda.synchronize()
+        return results
+    for _ in range(5):
+        for a, b in zip(run(True), run(False)):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
