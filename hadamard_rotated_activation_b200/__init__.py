@@ -5,7 +5,9 @@ Thin ctypes binding over the C ABI in include/kq.h (libkq.so, built in-tree by
 names and only marshal arguments: torch CUDA tensors become device pointers and
 the current torch stream becomes the kq stream.  Every step of the path runs in
 the library's CUDA kernels; there is no other implementation here, and a
-missing library is an error.
+missing library is an error.  The decode-step calls, which are short, are
+marshalled by a small extension module (csrc/kq_call.c) when nothing is wrong
+with their arguments, and by the functions below otherwise.
 
 PyTorch is used for device memory and streams only.
 """
@@ -302,7 +304,32 @@ def kq_gemm_nvfp4(a_codes, a_scales, a_tensor_scale, b_codes, b_scales, b_tensor
 
 # ------------------------------------------------- decode-step operators
 # These calls are short (a few microseconds of GPU work), so their marshalling
-# asks each tensor only what the kernels rely on.
+# asks each tensor only what the kernels rely on, and a native module does it
+# for calls that are right: it returns the status, or None, having called
+# nothing, for all others.
+_call = None
+
+
+def _native():
+    """The marshalling module, loaded and told of the library (once)."""
+    global _call
+    if _call is None:
+        import importlib
+        L, torch = lib(), _torch()
+        try:
+            mod = importlib.import_module("._kq_call", __name__)
+        except ImportError as e:
+            raise RuntimeError(
+                f"the _kq_call extension module is missing ({e}): build it with "
+                "`python -m hadamard_rotated_activation_b200.build`") from e
+        mod.init(torch.bfloat16, torch.float32, torch.float16, torch.uint8, torch.int8,
+                 torch.int32, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
+                 *[ctypes.cast(f, ctypes.c_void_p).value
+                   for f in (L.kq_gemv, L.kq_attn_decode_int4_kv, L.kq_kv_copy_pages)])
+        _call = mod
+    return _call
+
+
 def _want(t, what: str, dtype, shape, index: int) -> int:
     """Device pointer of a contiguous tensor of this type and shape on device
     `index`; ValueError for anything else.  The kernels take sizes from the
@@ -350,6 +377,15 @@ def kq_gemv(fmt: int, x, codes, scales, zeros, tensor_scale, group: int, y,
             stream=None) -> None:
     """y = x W^T for a few tokens: x [m, k] (m <= KQ_GEMV_MAX_TOKENS), W [n, k]
     in a 4-bit format as kq_dequant takes it, y [m, n]; x and y fp32 or bf16."""
+    status = (_call or _native()).gemv(fmt, x, codes, scales, zeros, tensor_scale, group, y,
+                                       stream)
+    if status is None:
+        _gemv_checked(fmt, x, codes, scales, zeros, tensor_scale, group, y, stream)
+    elif status != KQ_OK:
+        raise KQError(status, "kq_gemv")
+
+
+def _gemv_checked(fmt, x, codes, scales, zeros, tensor_scale, group, y, stream) -> None:
     torch = _torch()
     if x.dim() != 2 or codes.dim() != 2:
         raise ValueError("x is [m, k] and codes are [n, k/2]")
@@ -380,10 +416,15 @@ class KVCacheInt4:
     cache of several layers.  A view of the caller's tensors, checked
     once (so they cannot be exchanged)."""
 
-    __slots__ = ("_arrays", "layers", "num_slots", "dim", "index", "layered")
-    codes = property(lambda self: self._arrays[0])
-    scales = property(lambda self: self._arrays[1])
-    zeros = property(lambda self: self._arrays[2])
+    __slots__ = ("_view",)
+    codes = property(lambda self: self._view[0])
+    scales = property(lambda self: self._view[1])
+    zeros = property(lambda self: self._view[2])
+    layers = property(lambda self: self._view[3])
+    num_slots = property(lambda self: self._view[4])
+    dim = property(lambda self: self._view[5])
+    index = property(lambda self: self._view[6])
+    layered = property(lambda self: self._view[7])
 
     def __init__(self, codes, scales, zeros):
         torch = _torch()
@@ -395,10 +436,9 @@ class KVCacheInt4:
         _want(codes, "codes", torch.uint8, lead + (half,), at)
         _want(scales, "scales", torch.float16, lead + (half // 64,), at)
         _want(zeros, "zeros", torch.float16, lead + (half // 64,), at)
-        self._arrays = (codes, scales, zeros)
-        self.layered = len(lead) == 2
-        self.layers = lead[0] if self.layered else 1
-        self.num_slots, self.dim, self.index = lead[-1], 2 * half, at
+        layered = len(lead) == 2
+        self._view = (codes, scales, zeros, lead[0] if layered else 1, lead[-1], 2 * half, at,
+                      layered)
 
     def layer(self, i: int) -> "KVCacheInt4":
         """Layer i as a cache of its own (views of the same memory)."""
@@ -414,6 +454,18 @@ def kq_attn_decode_int4_kv(q, k_cache: KVCacheInt4, v_cache: KVCacheInt4, k_sign
     out bf16 [batch, q_heads, 128], block_table int32 [batch, width], seq_lens
     int32 [batch]; window > 0 keeps the last `window` tokens and the first
     `sinks` ones visible.  workspace: empty_attn_workspace(...)."""
+    status = (_call or _native()).attn(q, k_cache, v_cache, k_signs, v_signs, block_table,
+                                       page_size, seq_lens, softmax_scale, out, workspace, window,
+                                       sinks, stream)
+    if status is None:
+        _attn_checked(q, k_cache, v_cache, k_signs, v_signs, block_table, page_size, seq_lens,
+                      softmax_scale, out, workspace, window, sinks, stream)
+    elif status != KQ_OK:
+        raise KQError(status, "kq_attn_decode_int4_kv")
+
+
+def _attn_checked(q, k_cache, v_cache, k_signs, v_signs, block_table, page_size, seq_lens,
+                  softmax_scale, out, workspace, window, sinks, stream) -> None:
     torch = _torch()
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q is [batch, q_heads, 128] and block_table [batch, width]")
@@ -432,7 +484,8 @@ def kq_attn_decode_int4_kv(q, k_cache: KVCacheInt4, v_cache: KVCacheInt4, k_sign
             _want(q, "q", torch.bfloat16, shape, at), batch, q_heads, dim // 128,
             None if k_signs is None else _want(k_signs, "k_signs", torch.int8, (dim,), at),
             None if v_signs is None else _want(v_signs, "v_signs", torch.int8, (dim,), at),
-            *[a.data_ptr() for a in k_cache._arrays], *[a.data_ptr() for a in v_cache._arrays],
+            *[a.data_ptr() for a in k_cache._view[:3]],
+            *[a.data_ptr() for a in v_cache._view[:3]],
             k_cache.num_slots, _want(block_table, "block_table", torch.int32, (batch, width), at),
             width, page_size, _want(seq_lens, "seq_lens", torch.int32, (batch,), at), window,
             sinks, softmax_scale, _want(out, "out", torch.bfloat16, shape, at),
@@ -443,6 +496,14 @@ def kq_kv_copy_pages(pairs, page_size: int, k_cache: KVCacheInt4,
                      v_cache: Optional[KVCacheInt4] = None, stream=None) -> None:
     """Copies pages of the cache(s): pairs int32 [n, 2] of (source, destination)
     page; pairs with a page outside the cache are skipped."""
+    status = (_call or _native()).copy(pairs, page_size, k_cache, v_cache, stream)
+    if status is None:
+        _copy_checked(pairs, page_size, k_cache, v_cache, stream)
+    elif status != KQ_OK:
+        raise KQError(status, "kq_kv_copy_pages")
+
+
+def _copy_checked(pairs, page_size, k_cache, v_cache, stream) -> None:
     if pairs.dim() != 2:
         raise ValueError("pairs are [n, 2]")
     at, n = k_cache.index, pairs.shape[0]
@@ -455,11 +516,10 @@ def kq_kv_copy_pages(pairs, page_size: int, k_cache: KVCacheInt4,
             raise ValueError("the key and value caches differ in shape")
         if v_cache.index != at:
             raise ValueError(f"the caches are not both on cuda:{at}")
-        values = [a.data_ptr() for a in v_cache._arrays]
+        values = [a.data_ptr() for a in v_cache._view[:3]]
     _launch((_lib or lib()).kq_kv_copy_pages, "kq_kv_copy_pages", at, stream,
             _want(pairs, "pairs", _torch().int32, (n, 2), at), n, page_size, k_cache.num_slots,
-            k_cache.layers, k_cache.dim, k_cache.codes.data_ptr(), k_cache.scales.data_ptr(),
-            k_cache.zeros.data_ptr(), *values)
+            k_cache.layers, k_cache.dim, *[a.data_ptr() for a in k_cache._view[:3]], *values)
 
 
 def kq_dequant(fmt: int, codes, scales, zeros, tensor_scale, tokens: int, dim: int,

@@ -1,9 +1,10 @@
-"""Build libkq.so in-tree with nvcc for sm_100a.
+"""Build libkq.so in-tree with nvcc for sm_100a, and the _kq_call module beside it.
 
     python -m hadamard_rotated_activation_b200.build [--verbose]
 
-Compiles every .cu file under csrc/ into one shared library next to this file.
-Rebuilds only when a source or header is newer than the library.
+Compiles every .cu file under csrc/ into one shared library next to this file, and
+csrc/kq_call.c (C, CPython API) into an extension module of the running Python.
+Rebuilds only when a source or header is newer than what it is built into.
 """
 from __future__ import annotations
 
@@ -12,12 +13,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libkq.so")
+CALL_SOURCE = os.path.join(CSRC, "kq_call.c")
+CALL = os.path.join(HERE, "_kq_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -47,14 +51,33 @@ def _deps():
             glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target, deps) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def build_call(force: bool = False) -> str:
+    """The marshalling module of the decode-step calls."""
+    if force or not _newer(CALL, [CALL_SOURCE, os.path.join(INCLUDE, "kq.h")]):
+        cc = shutil.which("gcc") or shutil.which("cc")
+        if not cc:
+            raise RuntimeError("no C compiler found")
+        tmp = f"{CALL}.{os.getpid()}.tmp"
+        subprocess.run([cc, "-O2", "-Wall", "-Wextra", "-shared", "-fPIC", "-fvisibility=hidden",
+                        "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-o", tmp,
+                        CALL_SOURCE], check=True)
+        os.replace(tmp, CALL)
+    return CALL
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    build_call(force)
     if not force and up_to_date():
         return LIB
     cmd = [nvcc_path(), *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC,
