@@ -43,8 +43,8 @@
 // asynchronous copies, one barrier a tile.  (Measured instead: bulk copies issued
 // lane by lane took 100 cycles each, 6500 a tile; extra warps for the copies
 // left the others 96 registers, which spilled; one CTA of 16 warps an SM, two warps a
-// head, rotated each query once an SM but waited at its barrier, 44.2 us.)  Stage rows are 32 bytes longer
-// than a multiple of 128, which keeps both fragment reads free of bank conflicts.
+// head, rotated each query once an SM but waited at its barrier, 44.2 us.)  Stage rows
+// are 32 bytes longer than a multiple of 128, which keeps both fragment reads free of bank conflicts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

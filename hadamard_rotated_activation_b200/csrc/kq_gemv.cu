@@ -18,8 +18,9 @@
 //          exactly, in full alignment (off by 2e-7); z - 8 takes the place of z.
 //   NVFP4  E2M1 codes by the hardware conversion, times the block's E4M3 scale:
 //          at most 6 significant bits, exact in fp16.
-//   MXFP4  likewise, the block's power of two taken relative to the largest of
-//          the row's four blocks in the group (exact down to 2^-23 of it).
+//   MXFP4  up to 8 columns: the block's sum leaves the tensor core and takes its power
+//          of two in fp32.  More: as NVFP4, the power of two taken relative to the
+//          largest of the row's four blocks in the group (exact down to 2^-23 of it).
 // x is held per token and group of 128 as fp16 with a power of two that puts its
 // largest element in [2^14, 2^15), or in [1, 2) beside E2M1 codes (whose block sums
 // must not overflow): bf16 rows are exact down to 2^-31 or 2^-17 of it, and off by
@@ -31,11 +32,11 @@
 // CTAs of a cluster share the rows, split k between them and join their sums through
 // distributed shared memory in a fixed order, so there is no workspace and one
 // launch.  Measured (one B200, time between calls in a graph), INT4 asymmetric:
-// 4096 x 4096 by 1 token 5.2 us, 12288 x 4096 by 8 tokens 12.0 us; MXFP4 32003 x 4096
-// by 4 tokens 22.4 us = 3.1 TB/s; NVFP4 4096 x 12288 by 2 fp32 tokens 10.0 us.  Of
-// the 12.0 us about 2 are the launch, 1 the start, 2 staging x (which every CTA does
+// 4096 x 4096 by 1 token 5.0 us, 12288 x 4096 by 8 tokens 11.9 us; MXFP4 32003 x 4096
+// by 4 tokens 21.9 us = 3.2 TB/s; NVFP4 4096 x 12288 by 2 fp32 tokens 9.9 us.  Of
+// the 11.9 us about 2 are the launch, 1 the start, 2 staging x (which every CTA does
 // for its range of k), 4 the products at 1.9 instructions a cycle, 1 the cluster
-// barrier and 0.7 the join; with no copies at all it still takes 10.9.  Of the 22.4 us
+// barrier and 0.7 the join; with no copies at all it still takes 10.9.  Of the 21.9 us
 // 15.5 remain without the products, so there the memory and the instructions of the
 // E2M1 conversion and the block scales (about 120 a group and warp) share the bound.
 #include <cooperative_groups.h>
@@ -716,9 +717,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// CTAs that split k.  8 took the 4096 x 4096 product of one token from 6.3 to 6.6 us
-// (the cluster barrier), 2 the 12288 x 4096 one of eight from 14.6 to 16.2 (each CTA
-// stages more of x).
+// CTAs that split k.  Instead of 4, measured when these took 6.3 and 14.6 us: 8 took the
+// 4096 x 4096 product of one token to 6.6 (the cluster barrier), 2 the 12288 x 4096 one
+// of eight to 16.2 (each CTA stages more of x).
 constexpr int kSplit = 4;
 
 // Shared memory of a CTA: the stages, x of a segment, the sums.
