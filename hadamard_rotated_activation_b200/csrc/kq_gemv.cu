@@ -59,7 +59,7 @@ using sm100::pow2f;
 // A warp streams its rows in steps of 16 rows by kStep groups, kStages of which are
 // on their way or in use.  One tile of 8 columns: two CTAs of 8 warps an SM.  More:
 // one CTA of 16 warps, which stages x once an SM, and shorter steps, which leave x
-// and the sums more room (32000 x 4096 by 16 tokens took 79 us with two CTAs).
+// and the sums more room (32000 x 4096 by 16 tokens takes 34 us and took 79 with two CTAs).
 template <int NT>
 struct Shape {
   static constexpr int kWarps = NT == 1 ? 8 : 16;
@@ -273,9 +273,13 @@ __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, const E
   }
 }
 
-// First group of a rank (ranks is a power of two).
+// First group of a rank (ranks is a power of two): whole steps, so that the scales of a
+// step's row are an aligned copy wherever the row's are.
+template <int NT>
 __device__ __forceinline__ int rank_begin(const Params& P, int rank) {
-  return (int)((uint32_t)(rank * P.groups) >> P.rank_shift);
+  constexpr int kStep = Shape<NT>::kStep;
+  const uint32_t steps = (uint32_t)(P.groups + kStep - 1) / kStep;
+  return min((int)(rank * steps >> P.rank_shift) * kStep, P.groups);
 }
 
 // Whether a format's blocks are summed one by one (MXFP4 with few columns): a
@@ -581,7 +585,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   const int all_tiles = (int)min((int64_t)P.tiles, (P.n - first_row + 15) >> 4);
   const int own = (P.round + ranks - 1) >> P.rank_shift;  // tiles of a round a CTA owns at most
   const int mt = P.m, parts = P.parts;
-  const int gbegin = rank_begin(P, rank), gend = rank_begin(P, rank + 1);
+  const int gbegin = rank_begin<NT>(P, rank), gend = rank_begin<NT>(P, rank + 1);
   // rounds: as many tiles as the sums have room for
   for (int t0 = 0; t0 < all_tiles; t0 += P.round) {
     const int tiles = min(P.round, all_tiles - t0);
@@ -717,10 +721,22 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// CTAs that split k.  Instead of 4, measured when these took 6.3 and 14.6 us: 8 took the
-// 4096 x 4096 product of one token to 6.6 (the cluster barrier), 2 the 12288 x 4096 one
-// of eight to 16.2 (each CTA stages more of x).
-constexpr int kSplit = 4;
+// What a CTA's work costs, in instructions of a warp (of two CTAs on an SM, its half):
+// a step of a tile, a turn of staging x, a cluster's barriers, a further round of tiles.
+// The number of CTAs that split k is the one with the least sum.  Measured, bf16 tokens,
+// one rank against two: 1024 x 1024 by 1 token 3.2 and 3.5 us (one turn of staging
+// either way), by 8 tokens 4.6 and 4.1; 32000 x 1536 by 8 tokens 11.5 and 13.2 (three
+// steps are not halved).  Two against four: 4096 x 2048 by 16 tokens 8.0 and 7.5, 32000 x
+// 2048 19.9 and 29.5 (two rounds and four; one rank, one round: 18.1).  8 ranks, which
+// took the 4096 x 4096 product of one token from 6.3 to 6.6 us and the 12288 x 4096 one
+// of eight from 11.8 to 13.3, only where x has no room otherwise.
+template <int NT>
+struct Cost {
+  static constexpr int kStep = Shape<NT>::kStep * (60 + 40 * NT);
+  static constexpr int kTurn = Shape<NT>::kWarps * 90, kTurnF32 = Shape<NT>::kWarps * 150;
+  static constexpr int kBarrier = 1300 / Shape<NT>::kCtas;
+  static constexpr int kRound = 13000 / Shape<NT>::kCtas;
+};
 
 // Shared memory of a CTA: the stages, x of a segment, the sums.
 template <int NT>
@@ -772,29 +788,45 @@ template <int FMT, int NT, bool SMALL>
 cudaError_t launch(Params P, cudaStream_t s) {
   using R = Room<NT>;
   constexpr int kStep = Shape<NT>::kStep;
-  int ranks = 1;
-  while (ranks < kSplit && P.groups / (2 * ranks) >= kStep) ranks *= 2;
-  while (ranks < 8 && P.groups > ranks * R::kGroups) ranks *= 2;
+  const int64_t all = (P.n + 15) / 16;
+  const int steps_all = (P.groups + kStep - 1) / kStep;
+  auto groups_of = [&](int ranks) { return (steps_all + ranks - 1) / ranks * kStep; };
+  const int room = R::kSums / (P.m * 64);               // tiles times parts, and a rank's rounding
+  int ranks = 0;
+  int64_t tiles = 0, least = 0;
+  for (int r = 1; r <= 8; r *= 2) {
+    if (r > 1 && P.groups < r * kStep) break;
+    if (r < 8 ? groups_of(r) > R::kGroups : ranks > 0) continue;
+    int ctas = 0;
+    const cudaError_t e = resident_ctas<FMT, NT, SMALL>(r, &ctas);
+    if (e != cudaSuccess) return e;
+    // rows for as many clusters as run at a time
+    const int clusters = ctas / r;
+    const int64_t t = (all + clusters - 1) / clusters, rounds = (t + room - r) / (room - r + 1);
+    const int64_t turns = (P.m * groups_of(r) + Shape<NT>::kThreads / 16 - 1) /
+                          (Shape<NT>::kThreads / 16);
+    const int64_t cost = t * (groups_of(r) / kStep) * Cost<NT>::kStep +
+                         turns * (P.x_bf16 ? Cost<NT>::kTurn : Cost<NT>::kTurnF32) +
+                         (r > 1 ? Cost<NT>::kBarrier : 0) + (rounds - 1) * Cost<NT>::kRound;
+    if (ranks == 0 || cost < least) {
+      ranks = r;
+      tiles = t;
+      least = cost;
+    }
+  }
   P.ranks = ranks;
   for (P.rank_shift = 0; 1 << P.rank_shift < ranks;) ++P.rank_shift;
-  int ctas = 0;
-  cudaError_t e = resident_ctas<FMT, NT, SMALL>(ranks, &ctas);
-  if (e != cudaSuccess) return e;
-  const int64_t all = (P.n + 15) / 16;
   // x of a CTA's groups in one piece where there is room
-  const int mine = (P.groups + ranks - 1) / ranks;
-  P.seg = (mine + kStep - 1) / kStep * kStep;
+  P.seg = groups_of(ranks);
   if (P.seg > R::kGroups) P.seg = R::kGroups;
   P.recip = (65536u + P.m - 1) / P.m;
-  // a step's scales of a row are one or two aligned copies where every range and
-  // row begins at a multiple of kStep groups
+  // a step's scales of a row are one or two aligned copies where every row begins at a
+  // multiple of kStep groups
   const uintptr_t at = reinterpret_cast<uintptr_t>(P.scales) | reinterpret_cast<uintptr_t>(P.zeros);
-  P.wide = P.groups % (kStep * ranks) == 0 && P.k % 128 == 0 &&
+  P.wide = P.groups % kStep == 0 && P.k % 128 == 0 &&
            at % (FMT == KQ_FMT_INT4_ASYM ? 2 * kStep : FMT == KQ_FMT_NVFP4 ? 16 : 4 * kStep) == 0;
-  // rows for as many clusters as run at a time, in rounds as far as their sums fit
-  const int clusters = ctas / ranks;
-  P.tiles = (int)((all + clusters - 1) / clusters);
-  const int room = R::kSums / (P.m * 64);               // tiles times parts, and a rank's rounding
+  // in rounds as far as the sums fit
+  P.tiles = (int)tiles;
   P.round = P.tiles;
   if (P.round > room - ranks + 1) {
     const int rounds = (P.tiles + room - ranks) / (room - ranks + 1);
@@ -816,7 +848,8 @@ cudaError_t launch(Params P, cudaStream_t s) {
   const size_t smem = R::kRings + (size_t)P.seg * NT * (2048 + 64) +
                       sizeof(float) * ranks * P.parts * own * 16 * P.m;
   if (smem > (size_t)R::kAll) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute((const void*)k_gemv<FMT, NT, SMALL>,
+  const cudaError_t e =
+      cudaFuncSetAttribute((const void*)k_gemv<FMT, NT, SMALL>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, R::kAll);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];

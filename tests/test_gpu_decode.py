@@ -952,3 +952,21 @@ def test_decode_calls_in_a_chain():
     for _ in range(5):
         for a, b in zip(run(True), run(False)):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", sorted(FMT))
+@pytest.mark.parametrize("n,k,m,xt", [
+    # one rank; two with steps of 2 and 1, 3 and 2; four with a short last step; none whole
+    (4800, 1536, 1, "bf16"), (500, 1536, 8, "bf16"), (500, 2560, 4, "f32"), (90, 2176, 8, "bf16"),
+    (90, 2688, 8, "bf16"), (70, 5504, 7, "f32"), (70, 640, 16, "f32"), (40000, 1536, 8, "bf16"),
+    (33000, 2048, 16, "bf16"), (33000, 896, 16, "f32"), (50, 12800, 16, "bf16")])
+def test_gemv_splits_of_k(fmt, n, k, m, xt):
+    """Numbers of 128-wide groups that the ranks of a cluster and the steps of a
+    warp do and do not divide, with few rows and with many."""
+    rng = np.random.default_rng(n + k + m)
+    w = _weights(rng, fmt, n, k)
+    x = torch.from_numpy(rng.standard_normal((m, k))).cuda().to(KIND[xt])
+    y = torch.empty((m, n), device="cuda")
+    _gemv(fmt, x, *w, y)
+    rows = np.unique(np.concatenate([np.arange(min(n, 40)), rng.integers(0, n, 60), [n - 1]]))
+    _check_some_rows(fmt, x.double().cpu().numpy(), w, y, rows)
