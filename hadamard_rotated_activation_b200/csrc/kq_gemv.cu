@@ -665,21 +665,48 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas) k_gemv(
         const int owner = tile & (ranks - 1);
         float* to = red + (((rank * parts + part) * own + (tile >> P.rank_shift)) * 16 + g) * mt;
         if (owner != rank) to = cg::this_cluster().map_shared_rank(to, owner);
-        // behind the first segment: on top of what the same lane put there
-        auto put = [&](float* at, float v) { *at = g0 > gbegin ? *at + v : v; };
+        // Two tokens a store where their number is even: 4-byte ones to other CTAs took a
+        // seventh of 4096 x 2048 by 16 tokens.  (Four, by trading halves between lanes,
+        // took as long as two.)
+        if (g0 == gbegin && P.x_bf16 && (mt & 1) == 0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (P.x_bf16) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tok = 8 * n + 2 * t + (e & 1);
-              if (tok < mt) put(to + 8 * (e >> 1) * mt + tok, acc[n][e]);
-            }
-          } else {
-            const int tok = 4 * n + t;
+          for (int n = 0; n < NT; ++n) {
+            const int tok = 8 * n + 2 * t;
             if (tok < mt) {
-              put(to + tok, acc[n][0] + acc[n][1]);
-              put(to + 8 * mt + tok, acc[n][2] + acc[n][3]);
+              *reinterpret_cast<float2*>(to + tok) = make_float2(acc[n][0], acc[n][1]);
+              *reinterpret_cast<float2*>(to + 8 * mt + tok) = make_float2(acc[n][2], acc[n][3]);
+            }
+          }
+        } else if (NT == 4 && gend - gbegin <= P.seg && !P.x_bf16 && (mt & 1) == 0) {
+          // lanes t and t ^ 1 trade: the even one keeps row g, the odd one row g + 8
+          const int odd = t & 1;
+          float* half = to + (odd ? 8 * mt : 0);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float v0 = acc[n][0] + acc[n][1], v1 = acc[n][2] + acc[n][3];
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+            const int tok = 4 * n + (t & 2);
+            if (tok < mt)
+              *reinterpret_cast<float2*>(half + tok) = odd ? make_float2(other, v1)
+                                                           : make_float2(v0, other);
+          }
+        } else {
+          // behind the first segment: on top of what the same lane put there
+          auto put = [&](float* at, float v) { *at = g0 > gbegin ? *at + v : v; };
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (P.x_bf16) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int tok = 8 * n + 2 * t + (e & 1);
+                if (tok < mt) put(to + 8 * (e >> 1) * mt + tok, acc[n][e]);
+              }
+            } else {
+              const int tok = 4 * n + t;
+              if (tok < mt) {
+                put(to + tok, acc[n][0] + acc[n][1]);
+                put(to + 8 * mt + tok, acc[n][2] + acc[n][3]);
+              }
             }
           }
         }

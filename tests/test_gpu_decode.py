@@ -970,3 +970,20 @@ def test_gemv_splits_of_k(fmt, n, k, m, xt):
     _gemv(fmt, x, *w, y)
     rows = np.unique(np.concatenate([np.arange(min(n, 40)), rng.integers(0, n, 60), [n - 1]]))
     _check_some_rows(fmt, x.double().cpu().numpy(), w, y, rows)
+
+
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["int4_asym", "mxfp4"])
+def test_gemv_every_number_of_tokens(fmt, xt):
+    """Sums travel between the CTAs of a cluster four, two or one at a time by
+    the number of tokens; 1536: two ranks, 4096: four, 128: one."""
+    rng = np.random.default_rng(3)
+    for k in (128, 1536, 4096):
+        w = _weights(rng, fmt, 333, k)
+        for m in range(1, 17):
+            x = torch.from_numpy(rng.standard_normal((m, k))).cuda().to(KIND[xt])
+            buf = torch.full((m * 333 + 64,), 7.0, device="cuda")
+            y = buf[32:32 + m * 333].view(m, 333)
+            _gemv(fmt, x, *w, y)
+            _check_gemv(fmt, x.double().cpu().numpy(), w, y)
+            assert (buf[:32] == 7).all() and (buf[-32:] == 7).all()
