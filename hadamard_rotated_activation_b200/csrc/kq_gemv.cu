@@ -32,13 +32,13 @@
 // CTAs of a cluster share the rows, split k between them and join their sums through
 // distributed shared memory in a fixed order, so there is no workspace and one
 // launch.  Measured (one B200, time between calls in a graph), INT4 asymmetric:
-// 4096 x 4096 by 1 token 5.0 us, 12288 x 4096 by 8 tokens 11.9 us; MXFP4 32003 x 4096
-// by 4 tokens 21.9 us = 3.2 TB/s; NVFP4 4096 x 12288 by 2 fp32 tokens 9.9 us.  Of
-// the 11.9 us about 2 are the launch, 1 the start, 2 staging x (which every CTA does
-// for its range of k), 4 the products at 1.9 instructions a cycle, 1 the cluster
-// barrier and 0.7 the join; with no copies at all it still takes 10.9.  Of the 21.9 us
-// 15.5 remain without the products, so there the memory and the instructions of the
-// E2M1 conversion and the block scales (about 120 a group and warp) share the bound.
+// 4096 x 4096 by 1 token 5.0 us, 12288 x 4096 by 8 tokens 11.1 us; MXFP4 32003 x 4096
+// by 4 tokens 21.4 us = 3.3 TB/s; NVFP4 4096 x 12288 by 2 fp32 tokens 9.9 us.  When the
+// second took 11.9 us, about 2 were the launch, 1 the start, 2 staging x (which every
+// CTA does for its range of k), 4 the products at 1.9 instructions a cycle, 1 the
+// cluster barrier and 0.7 the join; with no copies at all it took 10.9.  When the third
+// took 23.1, 15.5 remained without the products: there the memory and the instructions
+// of the E2M1 conversion and the block scales share the bound.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

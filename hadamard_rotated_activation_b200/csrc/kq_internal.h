@@ -47,7 +47,7 @@ cudaError_t take_gemm_errors(unsigned int* out);
 // kernel executes griddepcontrol.wait before it touches memory, and reads no input
 // through the read-only path, so nothing else changes.  `more` further attributes may follow in attr[1] ...  (In a stream, call
 // behind call, it takes 1.4 to 2.7 us off the decode-step operators: an INT4 product of
-// 12288 x 4096 by 8 tokens 14.4 to 11.9 us.)
+// 12288 x 4096 by 8 tokens 14.4 to 11.9 us then.)
 inline cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, size_t smem, cudaStream_t s,
                                            cudaLaunchAttribute* attr, int more = 0) {
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
