@@ -496,7 +496,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
     float fa[2], fz[2];                    // per column 2t, 2t + 1
     float m[2], ref[2], l[2], zs[4], o[8][4];
     int ev = 0;
-    bool fresh = false;                    // no tile of the unit seen yet
+    // no visible token of the unit seen yet: a tile whose pages lie outside the cache
+    // leaves m at -infinity, which would take the weights added behind it to zero
+    bool fresh = false;
     int segment = 0;
     while (w.left > 0) {
       // ---- the unit's query, rotated; lane (g, t) holds dimensions 32 t .. of column g
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
           for (int j = 0; j < 2; ++j) stop[j] = fmax3(stop[j], sc[mb][0][j], sc[mb][1][j]);
         if (fresh || __any_sync(0xffffffffu, fmaxf(stop[0], stop[1]) > (float)kSlack ||
                                                  vtop > (float)(1 << (15 - kSlack)))) {
-          fresh = false;
+          fresh = hidden == 0xffffffffu;
           float keep[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
