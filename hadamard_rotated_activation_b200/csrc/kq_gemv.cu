@@ -45,6 +45,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "kq.h"
 #include "kq_internal.h"
@@ -388,6 +389,17 @@ struct Stream {
   }
 };
 
+// 2^e for -127 <= e <= 128 as two factors.  With a group's sum c (0 or 2^-25 .. 2^27) and
+// a token's scale f, c near f rest leaves fp32's range on the way only where the
+// product does, whichever of the two scales is far from 1.
+struct Power {
+  float near, rest;
+};
+__device__ __forceinline__ Power power(int e) {
+  const int h = max(min(e, 100), -100);
+  return Power{pow2f(h), pow2f(e - h)};
+}
+
 // Adds a staged step: its first ng groups, times groups gl ... of the staged x.
 template <int FMT, int NT, bool SMALL>
 __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int ng, const uint4* xs,
@@ -402,35 +414,52 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
   constexpr int kDown = 8 * kScaleRow;            // from row g to row g + 8
   const uint4* xg = xs + gl * NT * 128 + lane;
   const float2* fg = xf + gl * NT * 8 + 2 * t;
-  auto group = [&](int i) {
+  // plain: sums of 2^(e - 127) c_b stay far inside fp32 (MXFP4 block by block)
+  auto group = [&](int i, auto plain) {
     if constexpr (BLOCKS) {
-      // block b: 8 codes a lane; 2^e c_b of the four blocks, then the token's scale
+      // block b: 8 codes a lane; 2^(e - 127) c_b of the four blocks, then the token's scale
       const uint32_t ea = *reinterpret_cast<const uint32_t*>(sca + 4 * i);
       const uint32_t eb = *reinterpret_cast<const uint32_t*>(sca + kDown + 4 * i);
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      const float4 f = *reinterpret_cast<const float4*>(fg);
+      auto block = [&](int b, float (&c)[4]) {
         const int at = piece<true>(g, 4 * i + b) + 4 * t;
         uint32_t fa[4], fb[4];
         e2m1_halves(*reinterpret_cast<const uint32_t*>(ca + at), fa);
         e2m1_halves(*reinterpret_cast<const uint32_t*>(ca + 8 * kRow + at), fb);
         const uint4 x = xg[b * 32];
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         mma16816(c, fa[0], fb[0], fa[1], fb[1], x.x, x.y);
         mma16816(c, fa[2], fb[2], fa[3], fb[3], x.z, x.w);
-        // 2^(e - 127); the smallest, e = 0, is subnormal
-        const float pa = __uint_as_float(max(ea >> (8 * b) << 24 >> 1, 0x00400000u));
-        const float pb = __uint_as_float(max(eb >> (8 * b) << 24 >> 1, 0x00400000u));
-        sum[0] = fmaf(pa, c[0], sum[0]);
-        sum[1] = fmaf(pa, c[1], sum[1]);
-        sum[2] = fmaf(pb, c[2], sum[2]);
-        sum[3] = fmaf(pb, c[3], sum[3]);
+      };
+      if constexpr (plain) {
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          block(b, c);
+          const float pa = __uint_as_float(ea >> (8 * b) << 24 >> 1);
+          const float pb = __uint_as_float(eb >> (8 * b) << 24 >> 1);
+          sum[0] = fmaf(pa, c[0], sum[0]);
+          sum[1] = fmaf(pa, c[1], sum[1]);
+          sum[2] = fmaf(pb, c[2], sum[2]);
+          sum[3] = fmaf(pb, c[3], sum[3]);
+        }
+        acc[0][0] = fmaf(f.x, sum[0], acc[0][0]);
+        acc[0][1] = fmaf(f.z, sum[1], acc[0][1]);
+        acc[0][2] = fmaf(f.x, sum[2], acc[0][2]);
+        acc[0][3] = fmaf(f.z, sum[3], acc[0][3]);
+      } else {
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          block(b, c);
+          const Power pa = power((int)(ea >> (8 * b) & 255u) - 127);
+          const Power pb = power((int)(eb >> (8 * b) & 255u) - 127);
+          acc[0][0] = fmaf(c[0] * pa.near * f.x, pa.rest, acc[0][0]);
+          acc[0][1] = fmaf(c[1] * pa.near * f.z, pa.rest, acc[0][1]);
+          acc[0][2] = fmaf(c[2] * pb.near * f.x, pb.rest, acc[0][2]);
+          acc[0][3] = fmaf(c[3] * pb.near * f.z, pb.rest, acc[0][3]);
+        }
       }
-      const float4 f = *reinterpret_cast<const float4*>(fg);
-      acc[0][0] = fmaf(f.x, sum[0], acc[0][0]);
-      acc[0][1] = fmaf(f.z, sum[1], acc[0][1]);
-      acc[0][2] = fmaf(f.x, sum[2], acc[0][2]);
-      acc[0][3] = fmaf(f.z, sum[3], acc[0][3]);
       return;
     }
     const int at = piece<false>(g, 4 * i + t);
@@ -444,6 +473,7 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
       for (int j = 0; j < 4; ++j) c[n][j] = 0.0f;
     uint32_t ma[2] = {0, 0}, mb[2] = {0, 0};
     float sa = 1.0f, sb = 1.0f, za = 0.0f, zb = 0.0f;
+    uint32_t ea = 0, eb = 0;                // MXFP4: the rows' largest block exponents
     if (FMT == KQ_FMT_INT4_ASYM) {
       const uint16_t* s16 = reinterpret_cast<const uint16_t*>(sca) + i;
       sa = half_value(s16[0]);
@@ -470,8 +500,8 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
     } else {
       // relative to the largest of the row's four blocks
       const uint32_t ba = sca[4 * i + t], bb = sca[kDown + 4 * i + t];
-      uint32_t ea = max(ba, __shfl_xor_sync(0xffffffffu, ba, 1));
-      uint32_t eb = max(bb, __shfl_xor_sync(0xffffffffu, bb, 1));
+      ea = max(ba, __shfl_xor_sync(0xffffffffu, ba, 1));
+      eb = max(bb, __shfl_xor_sync(0xffffffffu, bb, 1));
       ea = max(ea, __shfl_xor_sync(0xffffffffu, ea, 2));
       eb = max(eb, __shfl_xor_sync(0xffffffffu, eb, 2));
       auto down = [](uint32_t d) {        // 2^-d in both halves, 0 for d > 24
@@ -480,8 +510,6 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
       };
       ma[0] = ma[1] = down(ea - ba);
       mb[0] = mb[1] = down(eb - bb);
-      sa = __uint_as_float(ea ? ea << 23 : 0x00400000u);
-      sb = __uint_as_float(eb ? eb << 23 : 0x00400000u);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -530,25 +558,56 @@ __device__ __forceinline__ void compute_step(const uint8_t* stage, int gl, int n
         acc[n][1] = fmaf(f.z, c[n][1], acc[n][1]);
         acc[n][2] = fmaf(f.x, c[n][2], acc[n][2]);
         acc[n][3] = fmaf(f.z, c[n][3], acc[n][3]);
+      } else if (ea - 64u < 128u && eb - 64u < 128u) {
+        // c 2^(e - 127) stays far inside fp32
+        const float pa = __uint_as_float(ea << 23), pb = __uint_as_float(eb << 23);
+        acc[n][0] = fmaf(f.x, c[n][0] * pa, acc[n][0]);
+        acc[n][1] = fmaf(f.z, c[n][1] * pa, acc[n][1]);
+        acc[n][2] = fmaf(f.x, c[n][2] * pb, acc[n][2]);
+        acc[n][3] = fmaf(f.z, c[n][3] * pb, acc[n][3]);
       } else {
-        acc[n][0] = fmaf(c[n][0] * f.x, sa, acc[n][0]);
-        acc[n][1] = fmaf(c[n][1] * f.z, sa, acc[n][1]);
-        acc[n][2] = fmaf(c[n][2] * f.x, sb, acc[n][2]);
-        acc[n][3] = fmaf(c[n][3] * f.z, sb, acc[n][3]);
+        const Power pa = power((int)ea - 127), pb = power((int)eb - 127);
+        acc[n][0] = fmaf(c[n][0] * pa.near * f.x, pa.rest, acc[n][0]);
+        acc[n][1] = fmaf(c[n][1] * pa.near * f.z, pa.rest, acc[n][1]);
+        acc[n][2] = fmaf(c[n][2] * pb.near * f.x, pb.rest, acc[n][2]);
+        acc[n][3] = fmaf(c[n][3] * pb.near * f.z, pb.rest, acc[n][3]);
       }
     }
   };
-  if (NT == 1 && ng >= kStep) {           // whole steps without a branch between groups
+  // Exponents 64 .. 191 (the two top bits differ) in all four blocks of a row's group.
+  auto plain_scales = [](uint32_t a) { return a ^ a << 1; };
+  auto all_plain = [](uint32_t a) {
+    return (bool)__all_sync(0xffffffffu, (a & 0x80808080u) == 0x80808080u);
+  };
+  // whole steps without a branch between groups
+  bool whole = NT == 1 && ng >= kStep;
+  if constexpr (BLOCKS) {
+    static_assert(kStep == 4, "one load a row");
+    const uint4 a = *reinterpret_cast<const uint4*>(sca);
+    const uint4 b = *reinterpret_cast<const uint4*>(sca + kDown);
+    const uint32_t in = plain_scales(a.x) & plain_scales(a.y) & plain_scales(a.z) &
+                        plain_scales(a.w) & plain_scales(b.x) & plain_scales(b.y) &
+                        plain_scales(b.z) & plain_scales(b.w);
+    whole = all_plain(whole ? in : 0u);
+  }
+  if (whole) {
 #pragma unroll
-    for (int i = 0; i < kStep; ++i, xg += NT * 128, fg += NT * 8) group(i);
+    for (int i = 0; i < kStep; ++i, xg += NT * 128, fg += NT * 8) group(i, std::true_type{});
   } else if (NT == 1) {
+    const int n = min(ng, kStep);
 #pragma unroll 1
-    for (int i = 0; i < ng; ++i, xg += NT * 128, fg += NT * 8) group(i);
+    for (int i = 0; i < n; ++i, xg += NT * 128, fg += NT * 8) {
+      if (BLOCKS && !all_plain(plain_scales(*reinterpret_cast<const uint32_t*>(sca + 4 * i)) &
+                               plain_scales(*reinterpret_cast<const uint32_t*>(sca + kDown + 4 * i))))
+        group(i, std::false_type{});
+      else
+        group(i, std::true_type{});
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < kStep; ++i, xg += NT * 128, fg += NT * 8) {
       if (i >= ng) break;
-      group(i);
+      group(i, std::true_type{});
     }
   }
 }
