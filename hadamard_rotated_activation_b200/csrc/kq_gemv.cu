@@ -22,9 +22,9 @@
 //          of two in fp32.  More: as NVFP4, the power of two taken relative to the
 //          largest of the row's four blocks in the group (exact down to 2^-23 of it).
 // x is held per token and group of 128 as fp16 with a power of two that puts its
-// largest element in [2^14, 2^15), or in [1, 2) beside E2M1 codes (whose block sums
-// must not overflow): bf16 rows are exact down to 2^-31 or 2^-17 of it, and off by
-// at most 2^-25 of it below.
+// largest element in [2^14, 2^15): bf16 rows are exact down to 2^-31 of it, and off by at
+// most 2^-39 of it below (INT4 with a bf16 result, where every second pair is divided by
+// 16: 2^-27 and 2^-35).  The largest sum, of E2M1 codes with their block scales, is below 2^34.
 // fp32 rows are two columns, the rounded value and 2^11 times what it leaves.
 // A group's sum leaves the tensor core after 8 steps and is added in fp32.
 //
@@ -229,8 +229,8 @@ __device__ __forceinline__ void stage_x(const Params& P, int g0, int ng, const E
       for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int sh =
-          top > 0.0f ? min((PAIRS ? 141 : 127) - (int)(__float_as_uint(top) >> 23), 126) : 0;
+      // -113 to 126, -114 for an infinity
+      const int sh = top > 0.0f ? min(141 - (int)(__float_as_uint(top) >> 23), 126) : 0;
       const float up = pow2f(sh);
       float sum = 0.0f;
 #pragma unroll

@@ -317,7 +317,13 @@ KQ_API kq_status kq_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* a_scales,
  * bf16, or twice the tokens of fp32).  INT4 products for a bf16 y keep about 17
  * bits of their largest, all others about 22.
  *   x       [m, k] fp32 or bf16 (x_dtype), 0 <= m <= KQ_GEMV_MAX_TOKENS; m == 0
- *           is a no-op.  fp32 rows keep 22 significant bits.
+ *           is a no-op.  Relative to the largest element of a token's 128 columns
+ *           (group), bf16 elements are exact down to 2^-31 and off by at most 2^-39
+ *           below, and fp32 elements keep 22 significant bits down to 2^-28 and are
+ *           off by at most 2^-50 below (INT4 products for a bf16 y: 2^-27 and 2^-35,
+ *           2^-24 and 2^-35).
+ *           An infinity or a NaN in a token's x makes all of its outputs infinite or
+ *           NaN, and those of no other token.
  *   codes   [n, k/2] bytes; scales, zeros, tensor_scale: as for kq_dequant with
  *           tokens = n and dim = k (block scales row-major).
  *   y       [m, n] fp32 or bf16 (y_dtype, rounded to nearest even).

@@ -1,6 +1,15 @@
 """GPU: kq_gemv where x, the weights' scales or both are near the ends of fp32's
 range, against the float64 oracle with the tolerance of tests/test_gpu_decode.py
 (nothing is required where the magnitudes that are added reach 2^127).
+
+To it comes what holding x in fp16 may take from elements far below their group's
+largest, as include/kq.h states it.  A group (a token's 128 columns) is held times a
+power of two that puts its largest element T in [2^14, 2^15).  fp16 steps by 2^-24
+below 2^-14, so an element is off by at most 2^-25 there, which is 2^-39 T; by 16
+times that, 2^-35 T, for INT4 with a bf16 result, where it is halved four times
+before it is rounded.  (Where fp32 elements are two parts, the second is 2^11 times
+what the first left, rounded the same way: 2^-50 T.)  Each weight w of the group takes
+|w| times as much into the result.
 """
 import numpy as np
 import pytest
@@ -8,7 +17,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import hadamard_rotated_activation_b200 as kq
-from test_gpu_decode import KIND, _check_gemv, _gemv, _weights
+from oracle import decode as od
+from test_gpu_decode import KIND, _gemv, _magnitude, _weights
 
 pytestmark = pytest.mark.gpu
 
@@ -29,7 +39,20 @@ def _tokens(rng, m, k, powers, xt):
 def _run(fmt, x, w, yt="f32"):
     y = torch.full((x.shape[0], w[0].shape[0]), float("nan"), dtype=KIND[yt], device="cuda")
     _gemv(fmt, x, *w, y)
-    _check_gemv(fmt, x.double().cpu().numpy(), w, y)
+    x64, k = x.double().cpu().numpy(), x.shape[1]
+    matrix = od.weights(fmt, *w)
+    ref, mag = od.gemv(x64, matrix), _magnitude(fmt, x64, *w)
+    tol = (2.0 ** -18 + (k / 128 + 16) * 2.0 ** -23) * mag + k * 2.0 ** -149
+    step = 2.0 ** -35 if fmt.startswith("int4") and yt == "bf16" else \
+        2.0 ** -39 if x.dtype == torch.bfloat16 else 2.0 ** -50
+    for at in range(0, k, 128):
+        top = np.abs(x64[:, at:at + 128]).max(1, keepdims=True)
+        tol += step * top * np.abs(matrix[:, at:at + 128]).sum(1)
+    if yt == "bf16":
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    err = np.abs(y.double().cpu().numpy() - ref)
+    ok = (err <= tol) | (mag >= 2.0 ** 127)
+    assert ok.all(), f"worst {(err / tol)[~ok].max()} x tolerance, {(~ok).sum()} outputs"
     return y
 
 
@@ -60,3 +83,77 @@ def test_mxfp4_blocks_far_apart_in_a_group(xt, m):
     codes = codes.reshape(33, 8, 32).copy()
     codes[:, 0::4] = rng.integers(0, 2, (33, 2, 32)) * 8            # 0 and -0
     _run("mxfp4", x, (codes.reshape(33, 256), scales, None, None))
+
+
+def _e2m1_weights(rng, fmt, n, k):
+    """Small weights: products with 2^127 stay below 2^127."""
+    codes, scales, _, t = _weights(rng, fmt, n, k)
+    scales[:] = rng.integers(1, 9, scales.shape) if fmt == "nvfp4" else \
+        rng.integers(80, 100, scales.shape)
+    return codes, scales, None, t
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("xt,m", [("bf16", 3), ("bf16", 12), ("f32", 2), ("f32", 5), ("f32", 15)])
+def test_e2m1_largest_tokens(fmt, xt, m):
+    """Elements of 2^127 and of the type's largest value, one a token."""
+    rng = np.random.default_rng(m)
+    w = _e2m1_weights(rng, fmt, 50, 384)
+    x = torch.from_numpy(rng.standard_normal((m, 384))).cuda().to(KIND[xt])
+    for i in range(m):
+        x[i, 29 * i % 384] = (2.0 ** 127, -torch.finfo(KIND[xt]).max, -2.0 ** 127, 2.0 ** 126)[i % 4]
+    _run(fmt, x, w)
+    _run(fmt, x, w, "bf16")
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("m", [3, 12])
+@pytest.mark.parametrize("power", [15, 18, 24])
+def test_e2m1_small_elements_beside_a_large_one(fmt, m, power):
+    """bf16 elements of 8 significant bits beside one of 2^power that meets zero
+    weights: they are 2^-power of it, and exact."""
+    rng = np.random.default_rng(power)
+    codes, scales, _, t = _weights(rng, fmt, 40, 256)
+    codes[:, [0, 130]] = 0
+    x = torch.full((m, 256), 1 + 2.0 ** -7, device="cuda")
+    x[:, [0, 130]] = 2.0 ** power
+    _run(fmt, x.bfloat16(), (codes, scales, None, t))
+
+
+@pytest.mark.parametrize("fmt", ["int4_asym", "int4_sym", "mxfp4", "nvfp4"])
+@pytest.mark.parametrize("xt,yt", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
+@pytest.mark.parametrize("m", [3, 12])
+def test_infinities_and_nan_stay_in_their_token(fmt, xt, yt, m):
+    """A token with an infinity or a NaN has no finite result; the others have theirs,
+    bit by bit."""
+    rng = np.random.default_rng(m)
+    w = _weights(rng, fmt, 37, 512)
+    x = torch.from_numpy(rng.standard_normal((m, 512))).cuda().to(KIND[xt])
+    want = _run(fmt, x, w, yt)
+    bad = {0: float("inf"), 2: float("nan"), m - 1: -float("inf")}
+    for token, value in bad.items():
+        x[token, 100 * token % 512] = value
+    got = torch.zeros_like(want)
+    _gemv(fmt, x, *w, got)
+    for i in range(m):
+        if i in bad:
+            assert not torch.isfinite(got[i]).any()
+        else:
+            assert torch.equal(got[i], want[i])
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("m", [2, 12])
+def test_e2m1_infinities_have_their_sign(fmt, m):
+    """bf16 x of one infinity, weights that are not zero there."""
+    rng = np.random.default_rng(m)
+    codes, scales, _, t = _weights(rng, fmt, 37, 256)
+    scales[scales == 0] = 1
+    codes[:, 77] = rng.integers(1, 8, 37) + 8 * rng.integers(0, 2, 37)
+    scales[:, 77 // (16 if fmt == "nvfp4" else 32)] = scales.max(1)
+    x = torch.zeros((m, 256), dtype=torch.bfloat16, device="cuda")
+    x[0, 77], x[1, 77] = float("inf"), -float("inf")
+    y = torch.zeros((m, 37), device="cuda")
+    _gemv(fmt, x, codes, scales, None, t, y)
+    sign = torch.from_numpy(np.where(codes[:, 77] < 8, np.inf, -np.inf)).float().cuda()
+    assert torch.equal(y[0], sign) and torch.equal(y[1], -sign) and not y[2:].any()
