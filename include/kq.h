@@ -322,8 +322,11 @@ KQ_API kq_status kq_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* a_scales,
  *           below, and fp32 elements keep 22 significant bits down to 2^-28 and are
  *           off by at most 2^-50 below (INT4 products for a bf16 y: 2^-27 and 2^-35,
  *           2^-24 and 2^-35).
- *           An infinity or a NaN in a token's x makes all of its outputs infinite or
- *           NaN, and those of no other token.
+ *           Where a group's largest element is neither 0 nor in [2^-100, 2^97], sums
+ *           in fp32 may leave its range before the scale of the row (INT4 symmetric)
+ *           or of the tensor (NVFP4) is applied, or lose bits (INT4); the result is
+ *           that of such sums then.  An infinity or a NaN in a token's x makes all of
+ *           its outputs infinite or NaN.  No token has a part in another's outputs.
  *   codes   [n, k/2] bytes; scales, zeros, tensor_scale: as for kq_dequant with
  *           tokens = n and dim = k (block scales row-major).
  *   y       [m, n] fp32 or bf16 (y_dtype, rounded to nearest even).

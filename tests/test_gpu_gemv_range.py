@@ -157,3 +157,64 @@ def test_e2m1_infinities_have_their_sign(fmt, m):
     _gemv(fmt, x, codes, scales, None, t, y)
     sign = torch.from_numpy(np.where(codes[:, 77] < 8, np.inf, -np.inf)).float().cuda()
     assert torch.equal(y[0], sign) and torch.equal(y[1], -sign) and not y[2:].any()
+
+
+@pytest.mark.parametrize("fmt", ["int4_asym", "int4_sym", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("xt,m,yt", [("bf16", 4, "f32"), ("bf16", 4, "bf16"), ("bf16", 12, "f32"),
+                                     ("bf16", 12, "bf16"), ("f32", 4, "f32"), ("f32", 6, "bf16"),
+                                     ("f32", 13, "f32"), ("f32", 13, "bf16")])
+def test_tokens_over_the_range_that_is_stated(fmt, xt, m, yt):
+    """Group maxima up to 2^97 and down to 2^-100, beside scales that take the result
+    the other way (and beside ordinary ones)."""
+    rng = np.random.default_rng(m)
+    for power, down in ([94, -60], [94, -14], [94, 0], [60, -90], [-60, 90], [-99, 60], [-99, 14],
+                        [-99, 0], [0, 100], [0, -100]):
+        codes, scales, zeros, t = _weights(rng, fmt, 60, 640)
+        if fmt == "int4_asym":
+            scales = np.ldexp(rng.uniform(0.5, 1, scales.shape),
+                              np.clip(down, -14, 15)).astype(np.float16)
+        elif fmt == "int4_sym":
+            scales = np.ldexp(rng.uniform(0.5, 1, 60),
+                              down + rng.integers(-9, 9, 60)).astype(np.float32)
+        elif fmt == "nvfp4":
+            t = np.float32(np.ldexp(0.7, down - 8))
+        else:
+            scales = (127 + down + rng.integers(-5, 5, scales.shape)).astype(np.uint8)
+        _run(fmt, _tokens(rng, m, 640, [power, power], xt).clamp(-2.0 ** 97, 2.0 ** 97),
+             (codes, scales, zeros, t), yt)
+
+
+@pytest.mark.parametrize("fmt", ["int4_asym", "int4_sym", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("n,k,m,xt", [(70, 4096, 5, "bf16"), (70, 2560, 11, "f32"),
+                                      (100, 32768, 16, "f32"), (40, 131072, 3, "bf16"),
+                                      (12007, 2048, 16, "bf16")])
+def test_far_groups_beside_near_ones(fmt, n, k, m, xt):
+    """Tokens whose groups are near 1, 2^80 and 2^-80 in turn along k: split over the
+    CTAs of a cluster, over segments of x and over rounds of rows."""
+    if fmt != "nvfp4":
+        n = min(n, 4000)
+    rng = np.random.default_rng(k)
+    w = _weights(rng, fmt, n, k)
+    x = rng.standard_normal((m, k // 512, 512))
+    for i in range(m):
+        x[i] *= np.exp2(rng.choice([0, 80, -80] if i % 3 == 0 else [0, -80] if i % 3 == 1 else [0],
+                                   k // 512))[:, None]
+    _run(fmt, torch.from_numpy(x.reshape(m, k)).cuda().to(KIND[xt]), w)
+
+
+@pytest.mark.parametrize("fmt", ["int4_sym", "nvfp4"])
+def test_zero_and_infinite_scales(fmt):
+    """A row's or the tensor's scale of zero, infinity or NaN reaches that row (all rows)
+    and no other."""
+    rng = np.random.default_rng(1)
+    codes, scales, _, t = _weights(rng, fmt, 40, 256)
+    x = _tokens(rng, 3, 256, [0, 90, -90], "bf16")
+    if fmt == "int4_sym":
+        scales[3], scales[17], scales[39] = 0, np.inf, np.nan
+        y = torch.empty((3, 40), device="cuda")
+        _gemv(fmt, x, codes, scales, None, t, y)
+        assert not y[:, 3].any() and y[:, 39].isnan().all() and not torch.isfinite(y[:, 17]).any()
+        scales[17] = scales[39] = 1
+        _run(fmt, x, (codes, scales, None, t))
+    else:
+        assert not _run(fmt, x, (codes, scales, None, np.float32(0))).any()
