@@ -413,8 +413,9 @@ class KVCacheInt4:
     """The three arrays of a paged INT4 cache (keys or values) as
     kq_rht_quant_int4_kv writes them: codes uint8 [num_slots, dim/2], scales
     and zeros fp16 [num_slots, dim/128]; with one more leading dimension a
-    cache of several layers.  A view of the caller's tensors, checked
-    once (so they cannot be exchanged)."""
+    cache of several layers.  A view of the caller's tensors, which have to stay
+    what they are: a call with a cache whose arrays were resized, or given other
+    memory of another shape, type or place since, is refused with ValueError."""
 
     __slots__ = ("_view",)
     codes = property(lambda self: self._view[0])
@@ -439,6 +440,14 @@ class KVCacheInt4:
         layered = len(lead) == 2
         self._view = (codes, scales, zeros, lead[0] if layered else 1, lead[-1], 2 * half, at,
                       layered)
+
+    def _addresses(self) -> list:
+        """Of the arrays; ValueError where one is not what the cache was made of."""
+        torch = _torch()
+        lead = (self.layers, self.num_slots) if self.layered else (self.num_slots,)
+        return [_want(self.codes, "codes", torch.uint8, lead + (self.dim // 2,), self.index),
+                _want(self.scales, "scales", torch.float16, lead + (self.dim // 128,), self.index),
+                _want(self.zeros, "zeros", torch.float16, lead + (self.dim // 128,), self.index)]
 
     def layer(self, i: int) -> "KVCacheInt4":
         """Layer i as a cache of its own (views of the same memory)."""
@@ -484,8 +493,7 @@ def _attn_checked(q, k_cache, v_cache, k_signs, v_signs, block_table, page_size,
             _want(q, "q", torch.bfloat16, shape, at), batch, q_heads, dim // 128,
             None if k_signs is None else _want(k_signs, "k_signs", torch.int8, (dim,), at),
             None if v_signs is None else _want(v_signs, "v_signs", torch.int8, (dim,), at),
-            *[a.data_ptr() for a in k_cache._view[:3]],
-            *[a.data_ptr() for a in v_cache._view[:3]],
+            *k_cache._addresses(), *v_cache._addresses(),
             k_cache.num_slots, _want(block_table, "block_table", torch.int32, (batch, width), at),
             width, page_size, _want(seq_lens, "seq_lens", torch.int32, (batch,), at), window,
             sinks, softmax_scale, _want(out, "out", torch.bfloat16, shape, at),
@@ -516,10 +524,10 @@ def _copy_checked(pairs, page_size, k_cache, v_cache, stream) -> None:
             raise ValueError("the key and value caches differ in shape")
         if v_cache.index != at:
             raise ValueError(f"the caches are not both on cuda:{at}")
-        values = [a.data_ptr() for a in v_cache._view[:3]]
+        values = v_cache._addresses()
     _launch((_lib or lib()).kq_kv_copy_pages, "kq_kv_copy_pages", at, stream,
             _want(pairs, "pairs", _torch().int32, (n, 2), at), n, page_size, k_cache.num_slots,
-            k_cache.layers, k_cache.dim, *[a.data_ptr() for a in k_cache._view[:3]], *values)
+            k_cache.layers, k_cache.dim, *k_cache._addresses(), *values)
 
 
 def kq_dequant(fmt: int, codes, scales, zeros, tensor_scale, tokens: int, dim: int,

@@ -5,7 +5,8 @@
 // status; for any other call it returns None, has called nothing, and the caller takes
 // the Python path, which says what is wrong (or changes the device).
 // (Time per call from Python: kq_gemv 8.4 to 4.5 us, the attention of short sequences 9.2
-// to 4.9, page copies 6.4 to 3.4; a launch alone takes about 2.9.)
+// to 4.9, page copies 6.4 to 3.4; a launch alone takes about 2.9.  Since then the caches'
+// arrays are asked again at every call: 1.4 us more for a pair of caches.)
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -150,7 +151,8 @@ static PyObject* gemv(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
 }
 
 // What a cache keeps of itself: (codes, scales, zeros, layers, num_slots, dim, index,
-// layered), checked when it was made.
+// layered).  The arrays are asked again at every call: they are the caller's, who may have
+// resized them or exchanged their memory since (0.7 us a cache).
 typedef struct {
   void* p[3];
   int64_t layers, slots, dim, at;
@@ -158,13 +160,20 @@ typedef struct {
 } Cache;
 static int cache_of(PyObject* o, Cache* c) {
   PyObject* v = PyObject_GetAttr(o, n_view);
-  int ok = v && PyTuple_CheckExact(v) && PyTuple_GET_SIZE(v) == 8;
-  for (int i = 0; ok && i < 3; ++i) ok = address(PyTuple_GET_ITEM(v, i), &c->p[i]);
-  ok = ok && as_int64(PyTuple_GET_ITEM(v, 3), &c->layers) &&
-       as_int64(PyTuple_GET_ITEM(v, 4), &c->slots) && as_int64(PyTuple_GET_ITEM(v, 5), &c->dim) &&
-       as_int64(PyTuple_GET_ITEM(v, 6), &c->at) && c->dim <= INT_MAX && c->layers <= INT_MAX &&
-       c->at >= 0;
-  if (ok) c->layered = PyTuple_GET_ITEM(v, 7) == Py_True;
+  int ok = v && PyTuple_CheckExact(v) && PyTuple_GET_SIZE(v) == 8 &&
+           as_int64(PyTuple_GET_ITEM(v, 3), &c->layers) &&
+           as_int64(PyTuple_GET_ITEM(v, 4), &c->slots) && as_int64(PyTuple_GET_ITEM(v, 5), &c->dim) &&
+           as_int64(PyTuple_GET_ITEM(v, 6), &c->at) && c->dim <= INT_MAX && c->layers <= INT_MAX &&
+           c->at >= 0;
+  if (ok) {
+    c->layered = PyTuple_GET_ITEM(v, 7) == Py_True;
+    int64_t shape[3] = {c->layers, c->slots, c->dim / 2};
+    const int skip = c->layered ? 0 : 1;
+    ok = want(PyTuple_GET_ITEM(v, 0), t_u8, 3 - skip, shape + skip, c->at, &c->p[0]);
+    shape[2] = c->dim / 128;
+    for (int i = 1; ok && i < 3; ++i)
+      ok = want(PyTuple_GET_ITEM(v, i), t_f16, 3 - skip, shape + skip, c->at, &c->p[i]);
+  }
   Py_XDECREF(v);
   return ok;
 }
