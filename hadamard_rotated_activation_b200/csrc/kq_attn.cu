@@ -77,6 +77,18 @@ constexpr int kUnitCost = 2;
 // 1024 10.3 (12.4) or 13.2 (14.4); 64 sequences of 128, 512 units, 13.0 or 16.6.
 constexpr int kAloneTokens = 512;
 constexpr int kPartFloats = kCols * 128 + 2 * kCols;   // o, m, l of one head
+// The workspace: partial sums of [CTA][first unit, last unit][head], then of each unit
+// the CTAs that worked on it.
+constexpr size_t kPartBytes = sizeof(float) * kMaxCtas * 2 * kWarps * kPartFloats;
+struct Span {
+  int first;                // 2 CTA + place of its partial sums
+  int last;                 // CTA
+};
+__device__ __forceinline__ Span* span_of(const AttnArgs& P, int64_t b, int blocks, int hb,
+                                         int chunks, int chunk) {
+  return reinterpret_cast<Span*>(static_cast<char*>(P.workspace) + kPartBytes) +
+         ((b * blocks + hb) * chunks + chunk);
+}
 
 // Tokens of one sequence: positions v < vis, v + skip from `sinks` on.
 struct Seq {
@@ -93,12 +105,6 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& P, int most, int64_t b) 
 __device__ __forceinline__ int longest(const AttnArgs& P) {
   const int64_t most = P.table_width * P.page_size;
   return most > 0x7fffffff ? 0x7fffffff : (int)most;
-}
-
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
 }
 
 // How `total` tiles are dealt: `ctas` contiguous ranges, the first `more` of
@@ -121,11 +127,6 @@ __device__ __forceinline__ Deal deal(int64_t total, int grid) {
 }
 __device__ __forceinline__ int64_t cta_first(const Deal& d, int c) {
   return c * d.each + min(c, d.more);
-}
-__device__ __forceinline__ int cta_of(const Deal& d, int64_t tile) {
-  const int64_t longer = (d.each + 1) * d.more;
-  return tile < longer ? (int)div64(tile, d.each + 1)
-                       : d.more + (int)div64(tile - longer, d.each);
 }
 
 // A walk over a CTA's tiles: sequence, block of heads, chunk of query heads, tile;
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the join, which reads the lengths ahead of its own wait: behind this one
+  // the join, whose CTAs may come in as soon as this kernel's leave room
   if (!ALONE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int most = longest(P);
   const int group = P.q_heads / P.kv_heads, chunks = (group + kCols - 1) / kCols;
@@ -787,6 +788,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
         }
       }
       const bool whole = todo == w.tiles;
+      if (!ALONE && threadIdx.x == 0) {      // for the join
+        Span* span = span_of(P, w.b, blocks, w.hb, chunks, w.chunk);
+        if (w.tile == 0) span->first = 2 * (int)blockIdx.x + (segment ? 1 : 0);
+        if (w.tile + todo == w.tiles) span->last = (int)blockIdx.x;
+      }
       if (part == 0) {
         if (whole) {
 #pragma unroll
@@ -823,7 +829,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn(AttnArgs P, PageDiv pages)
 // CTA order.
 constexpr int kRowWarps = 4;                  // warps with a row each, when there are many rows
 
-// Where the partial sums of a unit lie: `n` of them, from CTA c0 on.
+// Where the partial sums of a unit lie: `n` of them (one that is whole in its CTA has
+// none), from that CTA on.
 struct Parts {
   const float* base;
   int n, second;
@@ -832,29 +839,15 @@ struct Parts {
   }
 };
 template <int HB>
-__device__ __forceinline__ Parts parts_of(const AttnArgs& P, int grid, int64_t b, int kh, int chunk) {
-  constexpr int TILE = Shape<HB>::kTile;
+__device__ __forceinline__ Parts parts_of(const AttnArgs& P, int64_t b, int kh, int chunk) {
   const int chunks = (P.q_heads / P.kv_heads + kCols - 1) / kCols;
-  const int subs = P.kv_heads / HB * chunks, sub = kh / HB * chunks + chunk;
-  const int most = longest(P);
-  const int tiles = (sequence(P, most, b).vis + TILE - 1) / TILE;
-  int64_t before = 0, all = 0;
-  for (int64_t i = threadIdx.x & 31; i < P.batch; i += 32) {
-    const int vis = sequence(P, most, i).vis;
-    const int n = vis > 0 ? (vis + TILE - 1) / TILE + kUnitCost : 0;
-    all += n;
-    before += i < b ? n : 0;
-  }
-  const Deal dl = deal(warp_sum(all) * subs, grid);
-  const int64_t u0 = warp_sum(before) * subs + (int64_t)sub * (tiles + kUnitCost);
-  const int c0 = cta_of(dl, u0 + kUnitCost);
-  Parts p;
-  p.n = tiles > 0 ? cta_of(dl, u0 + kUnitCost + tiles - 1) - c0 + 1 : 0;
-  // CTA c0 has its second slot for this unit unless it begins with it
-  p.second = cta_first(dl, c0) < u0 ? 1 : 0;
-  p.base = static_cast<const float*>(P.workspace) +
-           ((int64_t)c0 * 2 * kWarps + kh % HB) * kPartFloats;
-  return p;
+  const Span span = *span_of(P, b, P.kv_heads / HB, kh / HB, chunks, chunk);
+  // a sequence without a visible token has no tile and no span
+  const bool any = sequence(P, longest(P), b).vis > 0;
+  const int c0 = span.first >> 1;
+  return Parts{static_cast<const float*>(P.workspace) +
+                   ((int64_t)c0 * 2 * kWarps + kh % HB) * kPartFloats,
+               any ? span.last - c0 + 1 : 0, span.first & 1};
 }
 
 // Maximum, sum and values (4 dimensions a lane) of column `col` over the partial
@@ -941,14 +934,14 @@ __device__ __forceinline__ void store_joined(const AttnArgs& P, float l, float4 
 // Many rows: a CTA takes (sequence, cached head, chunk of its query heads), a warp
 // a query head at a time.
 template <int HB>
-__global__ void __launch_bounds__(32 * kRowWarps) k_join_rows(AttnArgs P, int grid) {
+__global__ void __launch_bounds__(32 * kRowWarps) k_join_rows(AttnArgs P) {
   const int warp = threadIdx.x >> 5;
   const int group = P.q_heads / P.kv_heads, chunks = (group + kCols - 1) / kCols;
   const int64_t b = blockIdx.x;
   const int kh = blockIdx.y / chunks, chunk = blockIdx.y - kh * chunks;
-  const Parts p = parts_of<HB>(P, grid, b, kh, chunk);
-  const uint32_t signs = join_signs(P, kh);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Parts p = parts_of<HB>(P, b, kh, chunk);
+  const uint32_t signs = join_signs(P, kh);
   if (p.n < 2) return;
   const int columns = min(kCols, group - chunk * kCols);
   for (int col = warp; col < columns; col += kRowWarps) {
@@ -959,16 +952,16 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_join_rows(AttnArgs P, int gr
 
 // Fewer rows, which may have partial sums of many CTAs: a CTA takes one.
 template <int HB, int kJoinWarps>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_join_wide(AttnArgs P, int grid) {
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join_wide(AttnArgs P) {
   __shared__ float2 ml[kJoinWarps];
   __shared__ __align__(16) float red[kJoinWarps][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t b = blockIdx.x;
   const int qh = blockIdx.y, group = P.q_heads / P.kv_heads, kh = qh / group;
   const int chunk = (qh - kh * group) / kCols, col = (qh - kh * group) % kCols;
-  const Parts p = parts_of<HB>(P, grid, b, kh, chunk);
-  const uint32_t signs = warp == 0 ? join_signs(P, kh) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Parts p = parts_of<HB>(P, b, kh, chunk);
+  const uint32_t signs = warp == 0 ? join_signs(P, kh) : 0;
   if (p.n < 2) return;
   const Joined r = sum_parts<10>(p, col, warp, kJoinWarps);
   *reinterpret_cast<float4*>(&red[warp][4 * lane]) = r.v;
@@ -1051,22 +1044,21 @@ cudaError_t launch(const AttnArgs& P, int sms, cudaStream_t s) {
     const dim3 each((unsigned)P.batch, (unsigned)P.q_heads);
     const bool few = rows <= 2 * sms;
     cfg = dependent_launch(each, few ? 32 * 16 : 32 * 4, 0, s, attr);
-    return few ? cudaLaunchKernelEx(&cfg, k_join_wide<HB, 16>, P, grid)
-               : cudaLaunchKernelEx(&cfg, k_join_wide<HB, 4>, P, grid);
+    return few ? cudaLaunchKernelEx(&cfg, k_join_wide<HB, 16>, P)
+               : cudaLaunchKernelEx(&cfg, k_join_wide<HB, 4>, P);
   }
   const int chunks = (P.q_heads / P.kv_heads + kCols - 1) / kCols;
   cfg = dependent_launch(dim3((unsigned)P.batch, (unsigned)(P.kv_heads * chunks)),
                          32 * kRowWarps, 0, s, attr);
-  return cudaLaunchKernelEx(&cfg, k_join_rows<HB>, P, grid);
+  return cudaLaunchKernelEx(&cfg, k_join_rows<HB>, P);
 }
 
 }  // namespace at
 
 size_t attn_workspace_bytes(int64_t batch, int q_heads, int kv_heads) {
-  (void)batch;
-  (void)q_heads;
-  (void)kv_heads;
-  return sizeof(float) * (size_t)at::kMaxCtas * 2 * at::kWarps * at::kPartFloats;
+  // as many units as there are with one cached head each
+  const int64_t units = batch * kv_heads * ((q_heads / kv_heads + at::kCols - 1) / at::kCols);
+  return at::kPartBytes + sizeof(at::Span) * (size_t)(units + (units & 1));
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& args, cudaStream_t s) {
