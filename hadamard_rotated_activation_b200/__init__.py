@@ -306,8 +306,18 @@ def kq_gemm_nvfp4(a_codes, a_scales, a_tensor_scale, b_codes, b_scales, b_tensor
 # These calls are short (a few microseconds of GPU work), so their marshalling
 # asks each tensor only what the kernels rely on, and a native module does it
 # for calls that are right: it returns the status, or None, having called
-# nothing, for all others.
+# nothing, for all others (and for all calls where it was not built).
 _call = None
+
+
+class _PythonOnly:
+    """In place of the module where it was not built: every call is left to Python."""
+
+    @staticmethod
+    def gemv(*args):
+        return None
+
+    attn = copy = gemv
 
 
 def _native():
@@ -319,9 +329,12 @@ def _native():
         try:
             mod = importlib.import_module("._kq_call", __name__)
         except ImportError as e:
-            raise RuntimeError(
-                f"the _kq_call extension module is missing ({e}): build it with "
-                "`python -m hadamard_rotated_activation_b200.build`") from e
+            import warnings
+            warnings.warn(f"the _kq_call extension module is missing ({e}): decode-step calls take "
+                          "a few microseconds more; build it with "
+                          "`python -m hadamard_rotated_activation_b200.build`", RuntimeWarning)
+            _call = _PythonOnly
+            return _call
         mod.init(torch.bfloat16, torch.float32, torch.float16, torch.uint8, torch.int8,
                  torch.int32, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
                  *[ctypes.cast(f, ctypes.c_void_p).value

@@ -3,7 +3,8 @@
     python -m hadamard_rotated_activation_b200.build [--verbose]
 
 Compiles every .cu file under csrc/ into one shared library next to this file, and
-csrc/kq_call.c (C, CPython API) into an extension module of the running Python.
+csrc/kq_call.c (C, CPython API) into an extension module of the running Python, where
+there are a C compiler and Python's headers (the library needs neither).
 Rebuilds only when a source or header is newer than what it is built into.
 """
 from __future__ import annotations
@@ -62,17 +63,23 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
-def build_call(force: bool = False) -> str:
-    """The marshalling module of the decode-step calls."""
-    if force or not _newer(CALL, [CALL_SOURCE, os.path.join(INCLUDE, "kq.h")]):
-        cc = shutil.which("gcc") or shutil.which("cc")
-        if not cc:
-            raise RuntimeError("no C compiler found")
-        tmp = f"{CALL}.{os.getpid()}.tmp"
-        subprocess.run([cc, "-O2", "-Wall", "-Wextra", "-shared", "-fPIC", "-fvisibility=hidden",
-                        "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-o", tmp,
-                        CALL_SOURCE], check=True)
-        os.replace(tmp, CALL)
+def build_call(force: bool = False):
+    """The marshalling module of the decode-step calls; None (and no module) without a
+    C compiler or Python's headers, which only those calls' speed needs."""
+    if not force and _newer(CALL, [CALL_SOURCE, os.path.join(INCLUDE, "kq.h")]):
+        return CALL
+    cc = shutil.which("gcc") or shutil.which("cc")
+    headers = sysconfig.get_paths()["include"]
+    if not cc or not os.path.exists(os.path.join(headers, "Python.h")):
+        print("kq: no " + ("Python headers" if cc else "C compiler") + ", _kq_call is not built: "
+              "decode-step calls are marshalled by Python", file=sys.stderr)
+        if os.path.exists(CALL):              # of an older source
+            os.remove(CALL)
+        return None
+    tmp = f"{CALL}.{os.getpid()}.tmp"
+    subprocess.run([cc, "-O2", "-Wall", "-Wextra", "-shared", "-fPIC", "-fvisibility=hidden",
+                    "-I", INCLUDE, "-I", headers, "-o", tmp, CALL_SOURCE], check=True)
+    os.replace(tmp, CALL)
     return CALL
 
 
