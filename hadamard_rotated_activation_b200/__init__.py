@@ -463,7 +463,8 @@ class KVCacheInt4:
                 _want(self.zeros, "zeros", torch.float16, lead + (self.dim // 128,), self.index)]
 
     def layer(self, i: int) -> "KVCacheInt4":
-        """Layer i as a cache of its own (views of the same memory)."""
+        """Layer i as a cache of its own (views of the same memory) for the writing call
+        and the attention; page copies take the whole cache."""
         if not self.layered:
             raise ValueError("the cache has no layers")
         return KVCacheInt4(self.codes[i], self.scales[i], self.zeros[i])

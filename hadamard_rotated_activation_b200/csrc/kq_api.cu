@@ -418,10 +418,14 @@ KQ_API kq_status kq_attn_decode_int4_kv(
         (!k_codes || !k_scales || !k_zeros || !v_codes || !v_scales || !v_zeros))
       return KQ_ERR_INVALID_ARG;
   }
-  const void* wide[] = {q,        out,      workspace, k_signs, v_signs, k_codes,
-                        k_scales, k_zeros,  v_codes,   v_scales, v_zeros};
+  const void* wide[] = {q, out, workspace, k_signs, v_signs, k_codes, v_codes};
   for (const void* p : wide)
     if (!aligned(p, 16)) return KQ_ERR_MISALIGNED;
+  // scales of 8, 4, 2 or 1 heads at a time, whichever divides a row
+  const uintptr_t unit = 2 * (kv_heads % 8 == 0 ? 8 : kv_heads % 4 == 0 ? 4 : kv_heads % 2 == 0 ? 2 : 1);
+  const void* narrow[] = {k_scales, k_zeros, v_scales, v_zeros};
+  for (const void* p : narrow)
+    if (!aligned(p, unit)) return KQ_ERR_MISALIGNED;
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4)) return KQ_ERR_MISALIGNED;
   if (batch == 0) return KQ_OK;
   const kq::AttnArgs a{q,        batch,    q_heads, kv_heads,  k_signs,   v_signs,

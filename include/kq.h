@@ -366,8 +366,10 @@ KQ_API kq_status kq_gemv(int fmt, const void* x, int x_dtype, int64_t m, const u
  *   q, out        bf16 [batch, q_heads, 128], 16-byte aligned; no alias.
  *   k_signs, v_signs  int8 [kv_heads * 128] (the signs of the writing calls) or
  *                 NULL, 16-byte aligned.
- *   *_codes       [num_slots, kv_heads * 64] bytes; *_scales, *_zeros fp16
- *                 [num_slots, kv_heads]; all 16-byte aligned.
+ *   *_codes       [num_slots, kv_heads * 64] bytes, 16-byte aligned; *_scales,
+ *                 *_zeros fp16 [num_slots, kv_heads], aligned to 16, 8, 4 or 2 bytes,
+ *                 the first that divides 2 kv_heads (which every layer of an aligned
+ *                 [layers, num_slots, ...] array is).
  *   block_table   int32 [batch, table_width]; seq_lens int32 [batch] (4-byte
  *                 aligned, device memory).
  *   workspace     kq_attn_workspace_size(batch, q_heads, kv_heads) bytes of
