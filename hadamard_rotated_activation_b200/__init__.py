@@ -362,6 +362,13 @@ def _want(t, what: str, dtype, shape, index: int) -> int:
     raise ValueError(f"{what}: on cuda:{t.get_device()}, the call's tensors are on cuda:{index}")
 
 
+def _there(**arguments) -> None:
+    """ValueError for a missing tensor or cache."""
+    for name, a in arguments.items():
+        if a is None:
+            raise ValueError(f"{name}: missing")
+
+
 def _int32(**sizes) -> None:
     """ValueError for a size that the C entry's 32 bits would cut."""
     for name, v in sizes.items():
@@ -400,11 +407,12 @@ def kq_gemv(fmt: int, x, codes, scales, zeros, tensor_scale, group: int, y,
 
 def _gemv_checked(fmt, x, codes, scales, zeros, tensor_scale, group, y, stream) -> None:
     torch = _torch()
+    _there(x=x, codes=codes, y=y)
     if x.dim() != 2 or codes.dim() != 2:
         raise ValueError("x is [m, k] and codes are [n, k/2]")
     (m, k), n, at = x.shape, codes.shape[0], x.get_device()
-    if (k | group) >> 31:
-        _int32(k=k, group=group)
+    if (k | group | fmt) >> 31:
+        _int32(k=k, group=group, fmt=fmt)
     z = t = None
     if fmt == KQ_FMT_INT4_ASYM:
         s = _want(scales, "scales", torch.float16, (n, k // 128), at)
@@ -442,6 +450,7 @@ class KVCacheInt4:
 
     def __init__(self, codes, scales, zeros):
         torch = _torch()
+        _there(codes=codes)
         if codes.dim() not in (2, 3):
             raise ValueError("codes are [num_slots, dim/2] or [layers, num_slots, dim/2]")
         lead, half, at = tuple(codes.shape[:-1]), codes.shape[-1], codes.get_device()
@@ -490,6 +499,7 @@ def kq_attn_decode_int4_kv(q, k_cache: KVCacheInt4, v_cache: KVCacheInt4, k_sign
 def _attn_checked(q, k_cache, v_cache, k_signs, v_signs, block_table, page_size, seq_lens,
                   softmax_scale, out, workspace, window, sinks, stream) -> None:
     torch = _torch()
+    _there(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, workspace=workspace)
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q is [batch, q_heads, 128] and block_table [batch, width]")
     batch, q_heads, _ = q.shape
@@ -526,6 +536,7 @@ def kq_kv_copy_pages(pairs, page_size: int, k_cache: KVCacheInt4,
 
 
 def _copy_checked(pairs, page_size, k_cache, v_cache, stream) -> None:
+    _there(pairs=pairs, k_cache=k_cache)
     if pairs.dim() != 2:
         raise ValueError("pairs are [n, 2]")
     at, n = k_cache.index, pairs.shape[0]
