@@ -52,6 +52,7 @@
 #include <cstdint>
 
 #include "kq_internal.h"
+#include "kq_mma16.cuh"
 #include "kq_sm100.cuh"
 
 namespace kq {
@@ -66,7 +67,6 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSlack = 6;
 constexpr int kCols = 8;                      // query heads a unit carries
 constexpr int kMaxCtas = 320;
-constexpr int kMinTiles = 1;                  // tiles a CTA takes at least
 // What beginning a unit costs, in tiles: the query's rotation and the end of the
 // unit before it.  The tiles are dealt with so many more in front of each unit.
 constexpr int kUnitCost = 2;
@@ -119,8 +119,7 @@ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
 }
 __device__ __forceinline__ Deal deal(int64_t total, int grid) {
   Deal d;
-  const int64_t c = total / kMinTiles;
-  d.ctas = c < 1 ? 1 : c > grid ? grid : (int)c;
+  d.ctas = total < grid ? (int)total : grid;
   d.each = div64(total, d.ctas);
   d.more = (int)(total - d.each * d.ctas);
   return d;
@@ -216,7 +215,8 @@ __device__ __forceinline__ bool begin(const AttnArgs& P, int most, int blocks, i
   return false;
 }
 
-// pos / page_size for pos < 2^31 by a multiplication: with l = ceil(log2 d) and
+// pos / page_size for pos < 2^31 by a multiplication (Granlund and Montgomery, Division by
+// invariant integers using multiplication, 1994): with l = ceil(log2 d) and
 // M = ceil(2^(31 + l) / d), M d - 2^(31 + l) < d <= 2^l, so floor(pos M / 2^(31 + l))
 // is the quotient.  M = 0 stands for d = 1.
 struct PageDiv {
@@ -298,25 +298,10 @@ template <int N>
 __device__ __forceinline__ void wait_copies() {   // at most N groups still under way
   asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-               "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ float2 half2_floats(uint32_t h) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 __device__ __forceinline__ float exp2_(float x) {
   float y;
@@ -1072,7 +1057,10 @@ cudaError_t launch_attn_decode(const AttnArgs& args, cudaStream_t s) {
   const int64_t longest = P.table_width * P.page_size;
   if (units <= 2 * sms && (P.window > 0 && keep < longest ? keep : longest) <= at::kAloneTokens)
     return at::launch_alone(P, (int)units, s);
-  // the widest block of heads whose rows and scales stay whole
+  // The widest block of heads whose rows and scales stay whole.  (8 cached heads in blocks
+  // of 8, 4, 2, 1: 32 sequences of 300 to 4096 tokens 23.5, 24.8, 28.8, 33.8 us; 131071
+  // tokens 42.8, 43.0, 50.2, 55.5; 64 behind a window 27.7, 30.3, 37.7, 44.9.  Blocks of 2
+  // spill 32 bytes, the others nothing.)
   if (P.kv_heads % 8 == 0) return at::launch<8>(P, sms, s);
   if (P.kv_heads % 4 == 0) return at::launch<4>(P, sms, s);
   if (P.kv_heads % 2 == 0) return at::launch<2>(P, sms, s);

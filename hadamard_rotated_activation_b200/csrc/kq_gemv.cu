@@ -49,13 +49,14 @@
 
 #include "kq.h"
 #include "kq_internal.h"
+#include "kq_mma16.cuh"
 #include "kq_sm100.cuh"
 
 namespace kq {
 namespace gv {
 
 namespace cg = cooperative_groups;
-using sm100::pow2f;
+using namespace sm100;
 
 // A warp streams its rows in steps of 16 rows by kStep groups, kStages of which are
 // on their way or in use.  One tile of 8 columns: two CTAs of 8 warps an SM.  More:
@@ -92,13 +93,6 @@ struct Params {
   uint32_t recip;                         // 2^16 / m, rounded up
 };
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-               "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // Eight E2M1 codes -> four fp16 pairs, in the order of the codes.
 __device__ __forceinline__ void e2m1_halves(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
@@ -137,20 +131,12 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool i
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
                  :: "r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ float2 half2_floats(uint32_t h) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-
 // Eight INT4 codes (offset codes: symmetric ones with their sign bit turned) -> u - 8
 // as fp16 pairs (0,4) (1,5) (2,6) (3,7).
 template <bool TURN>
 __device__ __forceinline__ void code_halves(uint32_t w, uint32_t (&h)[4]) {
-  // 1024 + u and 1024 + 16 u, then - 1032 and / 16 - 72: every step is exact
+  // Integers below 2^10 placed under the exponent of 1024 (the usual way from bits to a
+  // floating-point number): 1024 + u and 1024 + 16 u, then - 1032 and / 16 - 72: every step is exact
   constexpr uint32_t lo = TURN ? 0x64086408u : 0x64006400u, hi = TURN ? 0x64806480u : 0x64006400u;
   const uint32_t v = w >> 8;
   h[0] = add_h2((w & 0x000f000fu) ^ lo, 0xe408e408u);

@@ -42,12 +42,11 @@ cudaError_t launch_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* a_scales,
                               int64_t n, int64_t k, void* c, int c_bf16, cudaStream_t s);
 cudaError_t take_gemm_errors(unsigned int* out);
 
-// Products of a few tokens with 4-bit weights (kq_gemv.cu).
 // A launch whose CTAs may be brought in while the kernel in front of it ends; the
 // kernel executes griddepcontrol.wait before it touches memory, and reads no input
-// through the read-only path, so nothing else changes.  `more` further attributes may follow in attr[1] ...  (In a stream, call
-// behind call, it takes 1.4 to 2.7 us off the decode-step operators: an INT4 product of
-// 12288 x 4096 by 8 tokens 14.4 to 11.9 us then.)
+// through the read-only path, so nothing else changes.  `more` further attributes may
+// follow in attr[1] ...  (In a stream, call behind call, it takes 1.4 to 2.7 us off the
+// decode-step operators: an INT4 product of 12288 x 4096 by 8 tokens 14.4 to 11.9 us then.)
 inline cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, size_t smem, cudaStream_t s,
                                            cudaLaunchAttribute* attr, int more = 0) {
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -62,6 +61,7 @@ inline cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, size_t smem, 
   return cfg;
 }
 
+// Products of a few tokens with 4-bit weights (kq_gemv.cu).
 cudaError_t launch_gemv(int fmt, const void* x, int x_bf16, int m, const uint8_t* codes,
                         const void* scales, const void* zeros, const float* tscale, int64_t n,
                         int k, void* y, int y_bf16, cudaStream_t s);
