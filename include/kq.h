@@ -380,9 +380,13 @@ KQ_API kq_status kq_gemv(int fmt, const void* x, int x_dtype, int64_t m, const u
  * q_heads / kv_heads <= 128, 1 <= page_size <= 65536, window and sinks >= 0,
  * softmax_scale finite, num_slots below 2^31, batch * table_width below 2^40,
  * batch <= 65535, batch * q_heads * min(table_width * page_size, 2^31) below 2^42.
- * batch == 0 is a no-op.  The query and the softmax weights are held in
- * fp16 with a power-of-two scale per head (relative rounding 2^-11) for the
- * tensor cores; scores, maxima, sums and the accumulated values in fp32.
+ * batch == 0 is a no-op.  For the tensor cores the rotated query is held in
+ * fp16 with a power-of-two scale per head, and so are the softmax weights times
+ * their token's value scale (both off by at most 2^-11 of themselves); scores,
+ * maxima, sums and the accumulated values in fp32.  Weights times scale (weights
+ * relative to the largest) that are below 2^-22 L, L the largest value scale among
+ * the visible tokens of the cached head, are off by at most 2^-33 L instead: a
+ * result that rests on tokens whose value scales are far below L has fewer bits.
  * Results do not depend on the order of execution.
  */
 KQ_API kq_status kq_attn_decode_int4_kv(
