@@ -21,9 +21,9 @@
 // heads that share the cached head, and at the memory's rate it needs 3/8 of
 // that path's throughput; the accumulators stay where the softmax is computed.
 // Measured (one B200, time between calls in a graph): one sequence of 131071
-// tokens, 8 cached and 64 query heads, 42.1 us = 3.4 TB/s, of which 30 us are the
+// tokens, 8 cached and 64 query heads, 42.7 us = 3.3 TB/s, of which 30 us are the
 // tiles, 6 the start (lengths, pages and query, one memory latency behind the other)
-// and 5 the join; 32 sequences of 300 to 4096 tokens 22.8 us.  In the tiles memory and
+// and 6 the join; 32 sequences of 300 to 4096 tokens 23.5 us.  In the tiles memory and
 // instruction issue are near each other: without the copies they take 25 us, at 1.9
 // to 2.0 instructions a cycle, half of them on the integer pipe (unpacking).
 //
@@ -32,10 +32,11 @@
 // ranges of equal length, computed on the device from seq_lens: long and short
 // sequences load the machine alike and nothing depends on host knowledge of
 // the lengths.  A unit that one CTA covers is finished there; the others leave
-// partial sums in the workspace, which a second small kernel (launched as a
-// programmatic dependent) joins in CTA order.  (Measured instead: a cooperative
-// launch that joins behind a barrier of the grid, 5 us slower in every case; the last
-// CTA of a unit to arrive, 47.6 for 24.5 us.)  Few and short sequences, by what the
+// partial sums in the workspace, and which CTAs they are, which a second small kernel
+// (launched as a programmatic dependent) joins in CTA order.  (Measured instead: the
+// join adding up the lengths again to find the CTAs, 1.2 to 1.6 us slower behind its
+// wait; a cooperative launch that joins behind a barrier of the grid, 5 us slower in
+// every case; the last CTA of a unit to arrive, 47.6 for 24.5 us.)  Few and short sequences, by what the
 // table and the window allow, are not cut: a CTA takes a unit, and nothing is joined.
 //
 // Per CTA: eight warps compute, each its own head (or its own part of the tokens
@@ -73,8 +74,9 @@ constexpr int kUnitCost = 2;
 // Where no sequence shows more tokens than this and every unit of one head finds a
 // CTA at once, a CTA takes a unit: no lengths to add up, nothing to join, one launch.
 // 4 sequences, 8 cached and 32 query heads, GPU time (time per call from the host),
-// dealt or alone: 256 tokens 8.0 (12.4) or 7.7 (10.2) us, 512 8.4 (12.4) or 9.6 (11.3),
-// 1024 10.3 (12.4) or 13.2 (14.4); 64 sequences of 128, 512 units, 13.0 or 16.6.
+// dealt or alone: 256 tokens 8.6 (9.8) or 7.5 (7.7) us, 512 9.2 (9.7) or 9.4 (9.4), 1024
+// 11.3 (11.7) or 13.3 (13.3); 37 sequences of 512, 296 units, 14.8 or 13.5; 64 of 128, 512
+// units, 13.0 or 16.6.
 constexpr int kAloneTokens = 512;
 constexpr int kPartFloats = kCols * 128 + 2 * kCols;   // o, m, l of one head
 // The workspace: partial sums of [CTA][first unit, last unit][head], then of each unit
@@ -838,7 +840,7 @@ __device__ __forceinline__ Parts parts_of(const AttnArgs& P, int64_t b, int kh, 
 // Maximum, sum and values (4 dimensions a lane) of column `col` over the partial
 // sums i0, i0 + by, ...; AHEAD of them are loaded at a time, with a running maximum.
 // (A CTA a row: 10, 131071 tokens 42.0 us and 42.7 with 4; a warp a row: 6, 64 windows of
-// 1028 tokens 27.4 us and 27.8 with 8 or 10.)
+// 1028 tokens 27.4 us and 27.8 with 8 or 10; both when finding the CTAs overlapped the wait.)
 struct Joined {
   float m, l;
   float4 v;

@@ -32,8 +32,8 @@
 // CTAs of a cluster share the rows, split k between them and join their sums through
 // distributed shared memory in a fixed order, so there is no workspace and one
 // launch.  Measured (one B200, time between calls in a graph), INT4 asymmetric:
-// 4096 x 4096 by 1 token 5.0 us, 12288 x 4096 by 8 tokens 11.1 us; MXFP4 32003 x 4096
-// by 4 tokens 21.4 us = 3.3 TB/s; NVFP4 4096 x 12288 by 2 fp32 tokens 9.9 us.  When the
+// 4096 x 4096 by 1 token 5.0 us, 12288 x 4096 by 8 tokens 11.2 us; MXFP4 32003 x 4096
+// by 4 tokens 21.3 us = 3.3 TB/s; NVFP4 4096 x 12288 by 2 fp32 tokens 9.9 us.  When the
 // second took 11.9 us, about 2 were the launch, 1 the start, 2 staging x (which every
 // CTA does for its range of k), 4 the products at 1.9 instructions a cycle, 1 the
 // cluster barrier and 0.7 the join; with no copies at all it took 10.9.  When the third

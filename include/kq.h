@@ -397,7 +397,8 @@ KQ_API kq_status kq_attn_decode_int4_kv(
     int64_t table_width, int page_size, const int32_t* seq_lens, int window, int sinks,
     float softmax_scale, void* out, void* workspace, size_t ws_bytes, kq_stream_t stream);
 
-/* Bytes of workspace kq_attn_decode_int4_kv needs (0 on bad arguments). */
+/* Bytes of workspace kq_attn_decode_int4_kv needs (0 on bad arguments): 21.3 MB and 8
+ * bytes for each sequence, cached head and 8 query heads that share it. */
 KQ_API size_t kq_attn_workspace_size(int64_t batch, int q_heads, int kv_heads);
 
 /*
